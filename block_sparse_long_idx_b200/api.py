@@ -36,8 +36,15 @@ class msa_kv2q_layout(ctypes.Structure):
                 ("counts", ctypes.c_size_t), ("bases", ctypes.c_size_t), ("total_bytes", ctypes.c_size_t)]
 
 
+class msa_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("B", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d_h", ctypes.c_int32),
+                ("L_max", ctypes.c_int64), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 _vp, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _LP = ctypes.POINTER(msa_kv2q_layout)
+_CP = ctypes.POINTER(msa_kv4_cache)
 
 # (name, restype, argtypes) for every symbol declared in include/msa.h
 SIGNATURES = [
@@ -64,6 +71,16 @@ SIGNATURES = [
     ("msa_quantize_e4m3", _int, [_vp, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp]),
     ("msa_sparse_prefill_fp8", _int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _int, _int,
                                       _vp, _LP, _vp, _vp, _vp, _vp, _sz, _vp]),
+    ("msa_kv4_rows_workspace_size", _sz, []),
+    ("msa_kv4_append", _int, [_CP, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    ("msa_kv4_read", _int, [_CP, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    ("msa_kv4_decode_workspace_size", _sz, [_int, _int]),
+    ("msa_kv4_decode", _int, [_CP, _vp, _vp, _int, _vp, _int, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _sz, _vp]),
+    ("msa_sparse_decode_kv4_workspace_size", _sz, [_int, _i64, _int, _int, _int, _int]),
+    ("msa_sparse_decode_kv4", _int, [_CP, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp, _vp, ctypes.c_float, _vp,
+                                     _vp, _vp, _vp, _sz, _vp]),
+    ("msa_kv4_evict_workspace_size", _sz, [_int, _int, _int]),
+    ("msa_kv4_evict", _int, [_CP, _CP, _vp, _vp, _int, _int, _int, _vp, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
     ("msa_selftest_workspace_size", _sz, []),
     ("msa_selftest_wait_timeout", _int, [_vp, _sz, _i64, _vp]),
     ("msa_trace_set", None, [_vp]),
@@ -72,7 +89,8 @@ SIGNATURES = [
 ]
 
 KERNEL_NAMES = {1: "index_topk", 2: "kv2q", 3: "attn", 4: "combine", 5: "dec_pool", 6: "dec_topk", 7: "dec_attn",
-                8: "dec_combine", 9: "bwd_prep", 10: "bwd_attn", 11: "bwd_convert", 12: "quant"}
+                8: "dec_combine", 9: "bwd_prep", 10: "bwd_attn", 11: "bwd_convert", 12: "quant",
+                13: "kv4_append", 14: "kv4_read", 15: "kv4_attn", 16: "kv4_weights", 17: "kv4_evict"}
 
 
 class msa_trace(ctypes.Structure):
@@ -412,3 +430,258 @@ def msa_sparse_prefill_fp8(q8: E4M3Rows, k8: E4M3Rows, v8: E4M3Rows, block_idx, 
         block_idx.data_ptr(), lp, _ptr(kv2q.buf) if kv2q is not None else None, out.data_ptr(), _ptr(lse),
         workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return out, lse
+
+
+# --------------------------------------------------------------------------- 4-bit key/value cache
+def _is(t, name, dtypes, shape, device):
+    """A contiguous CUDA tensor of one of `dtypes` and of `shape` on `device`, else ValueError."""
+    if not t.is_cuda or t.device != device or t.dtype not in dtypes or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected a contiguous {'/'.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)} "
+                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+class KV4Cache:
+    """A K/V cache held in 4 bits: E2M1 codes [B, H_kv, L_max, d_h / 2] uint8 (the even element in the low
+    nibble), one E4M3 scale per 16 elements [B, H_kv, L_max, d_h / 16] uint8, one fp32 scale per tensor.
+
+    L_max is a multiple of 128, d_h 64 or 128. The scales place the format's range: 16-element maxima
+    between 0.1 and 2688 times the scale keep full precision."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_scale: float = 1.0, v_scale: float = 1.0):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes: expected [B, H_kv, L_max, d_h / 2]")
+        B, H_kv, L_max, half = k_codes.shape
+        dev = k_codes.device
+        for t, n, last in ((k_codes, "k_codes", half), (k_scales, "k_scales", half // 8), (v_codes, "v_codes", half),
+                           (v_scales, "v_scales", half // 8)):
+            _is(t, n, (torch.uint8,), (B, H_kv, L_max, last), dev)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.B, self.H_kv, self.L_max, self.d_h, self.device = B, H_kv, L_max, 2 * half, dev
+        self._c = msa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), B, H_kv,
+                                2 * half, L_max, self.k_scale, self.v_scale)
+
+    @classmethod
+    def empty(cls, B: int, L_max: int, H_kv: int, d_h: int, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda"):
+        """A cache of uninitialised rows (rows are written by msa_kv4_append before lens covers them)."""
+        def rows(n):
+            return torch.empty((B, H_kv, L_max, n), dtype=torch.uint8, device=device)
+
+        return cls(rows(d_h // 2), rows(d_h // 16), rows(d_h // 2), rows(d_h // 16), k_scale, v_scale)
+
+
+class _Call:
+    """What a call of this section runs under: its tensors' device made current, the stream (the device's
+    current one unless given), and the memory that it allocates kept from reuse until that stream is done."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.own = stream is None
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard = None
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        self.handle = _stream(self.stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def hold(self, *tensors):
+        if self.own:
+            return
+        s = self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.handle, self.device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _tables(cache, T, starts, cu_seqlens):
+    _is(starts, "starts", _I32, (cache.B,), cache.device)
+    if cu_seqlens is not None:
+        _is(cu_seqlens, "cu_seqlens", _I32, (cache.B + 1,), cache.device)
+    elif T != cache.B:
+        raise ValueError("without cu_seqlens there is one row per sequence")
+
+
+def _token_stride(t, name, cache):
+    """Elements between the rows of t [T, H_kv, d_h], whose rows are contiguous."""
+    if (not t.is_cuda or t.device != cache.device or t.dtype not in _BF16 or t.dim() != 3 or
+            tuple(t.shape[1:]) != (cache.H_kv, cache.d_h) or t.stride(2) != 1 or
+            (cache.H_kv > 1 and t.stride(1) != cache.d_h)):
+        raise ValueError(f"{name}: expected a 16-bit tensor [T, {cache.H_kv}, {cache.d_h}] on {cache.device} whose rows are "
+                         f"contiguous, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else cache.H_kv * cache.d_h
+
+
+def msa_kv4_append(cache: KV4Cache, k, v, starts, cu_seqlens=None, workspace=None, stream=None):
+    """Quantises new rows k, v [T, H_kv, d_h] (bf16; the token stride is free) into the cache: the rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 go to the positions starts[b], starts[b] + 1, ... of sequence b;
+    without cu_seqlens T = B, one row per sequence. starts, cu_seqlens: int32 device tensors."""
+    T = k.shape[0]
+    ks, vs = _token_stride(k, "k", cache), _token_stride(v, "v", cache)
+    if v.shape[0] != T:
+        raise ValueError("k and v: different numbers of rows")
+    _tables(cache, T, starts, cu_seqlens)
+    with _Call(cache.device, stream) as call:
+        ws = _workspace(256, cache.device, workspace)
+        _check("msa_kv4_append", lib.msa_kv4_append(
+            ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), ks, vs, T, starts.data_ptr(), _ptr(cu_seqlens),
+            ws.data_ptr(), ws.numel(), call.handle))
+        call.hold(ws if workspace is None else None)
+
+
+def msa_kv4_read(cache: KV4Cache, starts, cu_seqlens=None, T: int | None = None, k=None, v=None, workspace=None,
+                 stream=None):
+    """The rows that msa_kv4_append with the same starts, cu_seqlens and T writes, as bf16 values.
+    Returns (k, v) [T, H_kv, d_h]."""
+    if T is None:
+        if cu_seqlens is not None:
+            raise ValueError("msa_kv4_read: T (the number of rows) is needed with cu_seqlens")
+        T = cache.B
+    _tables(cache, T, starts, cu_seqlens)
+    made = []
+    with _Call(cache.device, stream) as call:
+        for i, (t, n) in enumerate(((k, "k"), (v, "v"))):
+            if t is None:
+                made.append(torch.empty((T, cache.H_kv, cache.d_h), dtype=torch.bfloat16, device=cache.device))
+            else:
+                _is(t, n, _BF16, (T, cache.H_kv, cache.d_h), cache.device)
+        if k is None:
+            k = made[0]
+        if v is None:
+            v = made[-1]
+        ws = _workspace(256, cache.device, workspace)
+        _check("msa_kv4_read", lib.msa_kv4_read(
+            ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), T, starts.data_ptr(), _ptr(cu_seqlens), ws.data_ptr(),
+            ws.numel(), call.handle))
+        call.hold(ws if workspace is None else None, *made)
+    return k, v
+
+
+def _decode_tensors(q, cache, lens, out, lse, weights, weights_out):
+    if q.dim() != 3:
+        raise ValueError("q: expected [B, H_q, d_h]")
+    H_q = q.shape[1]
+    _is(q, "q", _BF16, (cache.B, H_q, cache.d_h), cache.device)
+    _is(lens, "lens", _I32, (cache.B,), cache.device)
+    if out is not None:
+        _is(out, "out", _BF16, q.shape, cache.device)
+    if lse is not None:
+        _is(lse, "lse", _F32, (cache.B, H_q), cache.device)
+    for t, n in ((weights, "weights"), (weights_out, "weights_out")):
+        if t is not None:
+            _is(t, n, _F32, (cache.B, cache.H_kv, cache.L_max), cache.device)
+    if weights is not None and weights_out is None:
+        raise ValueError("weights: give weights_out too (it may be the same tensor)")
+    return H_q
+
+
+def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weights_out=None, decay: float = 1.0, out=None,
+                   lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Attention of one query token per sequence (q [B, H_q, d_h]) over the first lens[b] rows of the 4-bit
+    cache, or over those of them in the blocks block_idx [B, H_kv, k] (ascending, -1 padded, 128 rows each).
+    With weights_out [B, H_kv, L_max] fp32 also weights_out = decay * weights + the group's attention
+    weights, at the visible positions. Returns (out, lse)."""
+    H_q = _decode_tensors(q, cache, lens, out, lse, weights, weights_out)
+    k = 0
+    if block_idx is not None:
+        if block_idx.dim() != 3:
+            raise ValueError("block_idx: expected [B, H_kv, k]")
+        k = block_idx.shape[2]
+        _is(block_idx, "block_idx", _I32, (cache.B, cache.H_kv, k), cache.device)
+    with _Call(cache.device, stream) as call:
+        made = []
+        if out is None:
+            made.append(out := torch.empty_like(q))
+        if lse is None and want_lse:
+            made.append(lse := torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device))
+        ws = _workspace(lib.msa_kv4_decode_workspace_size(cache.B, H_q), cache.device, workspace)
+        _check("msa_kv4_decode", lib.msa_kv4_decode(
+            ctypes.byref(cache._c), q.data_ptr(), lens.data_ptr(), H_q, _ptr(block_idx), k, _ptr(weights),
+            _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), call.handle))
+        call.hold(ws if workspace is None else None, *made)
+    return out, lse
+
+
+def msa_sparse_decode_kv4(q, q_idx, cache: KV4Cache, k_idx_cache, lens, B_k: int = 128, k: int = 16, weights=None,
+                          weights_out=None, decay: float = 1.0, out=None, lse=None, want_lse: bool = True,
+                          block_idx_out=None, workspace=None, stream=None):
+    """msa_sparse_decode with K and V in a 4-bit cache (the index keys k_idx_cache [B, L_max, H_kv, d_idx]
+    stay bf16); weights, weights_out and decay as for msa_kv4_decode. Returns (out, lse, block_idx)."""
+    H_q = _decode_tensors(q, cache, lens, out, lse, weights, weights_out)
+    if q_idx.dim() != 3:
+        raise ValueError("q_idx: expected [B, H_kv, d_idx]")
+    d_idx = q_idx.shape[2]
+    _is(q_idx, "q_idx", _BF16, (cache.B, cache.H_kv, d_idx), cache.device)
+    _is(k_idx_cache, "k_idx_cache", _BF16, (cache.B, cache.L_max, cache.H_kv, d_idx), cache.device)
+    if block_idx_out is not None:
+        _is(block_idx_out, "block_idx_out", _I32, (cache.B, cache.H_kv, k), cache.device)
+    with _Call(cache.device, stream) as call:
+        made = []
+        if out is None:
+            made.append(out := torch.empty_like(q))
+        if lse is None and want_lse:
+            made.append(lse := torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device))
+        if block_idx_out is None:
+            made.append(block_idx_out := torch.empty((cache.B, cache.H_kv, max(k, 0)), dtype=torch.int32, device=cache.device))
+        ws = _workspace(lib.msa_sparse_decode_kv4_workspace_size(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k),
+                        cache.device, workspace)
+        _check("msa_sparse_decode_kv4", lib.msa_sparse_decode_kv4(
+            ctypes.byref(cache._c), q.data_ptr(), q_idx.data_ptr(), k_idx_cache.data_ptr(), lens.data_ptr(), H_q, d_idx, B_k,
+            k, _ptr(weights), _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), block_idx_out.data_ptr(),
+            ws.data_ptr(), ws.numel(), call.handle))
+        call.hold(ws if workspace is None else None, *made)
+    return out, lse, block_idx_out
+
+
+def msa_kv4_evict(cache: KV4Cache, to: KV4Cache, weights, lens, keep: int, recent: int = 0, first: int = 0,
+                  weights_dst=None, k_idx_cache=None, k_idx_dst=None, lens_out=None, kept=None, workspace=None,
+                  stream=None):
+    """Copies the kept tokens of every (sequence, KV head) of `cache` to the front of `to`: the first `first`,
+    the last `recent` and, of the others, those with the largest weights [B, H_kv, L_max] (equal ones: the
+    lower position), `keep` in all, in their order; all of a sequence of at most `keep` tokens. weights_dst
+    [B, H_kv, to.L_max] and k_idx_dst [B, to.L_max, H_kv, d_idx] get the kept tokens' weights and index
+    keys. Returns (lens_out [B], kept [B, H_kv, keep] positions, -1 padded)."""
+    dev = cache.device
+    _is(weights, "weights", _F32, (cache.B, cache.H_kv, cache.L_max), dev)
+    _is(lens, "lens", _I32, (cache.B,), dev)
+    if to.device != dev:
+        raise ValueError("to: a cache on another device")
+    if weights_dst is not None:
+        _is(weights_dst, "weights_dst", _F32, (to.B, to.H_kv, to.L_max), dev)
+    if (k_idx_cache is None) != (k_idx_dst is None):
+        raise ValueError("give k_idx_cache and k_idx_dst together")
+    d_idx = 0
+    if k_idx_cache is not None:
+        d_idx = k_idx_cache.shape[-1]
+        _is(k_idx_cache, "k_idx_cache", _BF16, (cache.B, cache.L_max, cache.H_kv, d_idx), dev)
+        _is(k_idx_dst, "k_idx_dst", _BF16, (to.B, to.L_max, to.H_kv, d_idx), dev)
+    if lens_out is not None:
+        _is(lens_out, "lens_out", _I32, (cache.B,), dev)
+    if kept is not None:
+        _is(kept, "kept", _I32, (cache.B, cache.H_kv, keep), dev)
+    with _Call(dev, stream) as call:
+        made = []
+        if lens_out is None:
+            made.append(lens_out := torch.empty_like(lens))
+        if kept is None:
+            made.append(kept := torch.empty((cache.B, cache.H_kv, max(keep, 0)), dtype=torch.int32, device=dev))
+        ws = _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
+        _check("msa_kv4_evict", lib.msa_kv4_evict(
+            ctypes.byref(cache._c), ctypes.byref(to._c), weights.data_ptr(), lens.data_ptr(), keep, recent, first,
+            _ptr(k_idx_cache), _ptr(k_idx_dst), d_idx, _ptr(weights_dst), lens_out.data_ptr(), kept.data_ptr(),
+            ws.data_ptr(), ws.numel(), call.handle))
+        call.hold(ws if workspace is None else None, *made)
+    return lens_out, kept

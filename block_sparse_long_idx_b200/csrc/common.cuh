@@ -174,5 +174,7 @@ struct DecodeArgs {
     int* err;
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
+// Its index branch alone: pooled scores and Top-k into a.sel, a.nsel (and a.block_idx_out).
+cudaError_t launch_decode_index(const DecodeArgs& a, cudaStream_t s);
 
 } // namespace msa

@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(DecodeArgs a)
 
 } // namespace
 
-cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s)
+cudaError_t launch_decode_index(const DecodeArgs& a, cudaStream_t s)
 {
     const int nb_max = (int)((a.L_max + kBk - 1) / kBk);
     int dev = 0, n_sm = 148;
@@ -482,9 +482,16 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s)
     trace_begin(s);
     decode_topk_kernel<<<dim3(a.B, a.H_kv), 32, 0, s>>>(a, nb_max);
     trace_end(s, MSA_KERNEL_DEC_TOPK);
-    note_launch(4);
+    note_launch(3);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s)
+{
+    cudaError_t e = launch_decode_index(a, s);
+    if (e != cudaSuccess) return e;
+    note_launch(1);
     trace_begin(s);
-    cudaError_t e;
     if (a.d_h == 128) {
         e = cudaFuncSetAttribute(decode_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  DecCfg<128>::SMEM);

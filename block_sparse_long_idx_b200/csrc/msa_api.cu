@@ -6,10 +6,12 @@
 #include <mutex>
 
 #include <algorithm>
+#include <cmath>
 #include <vector>
 
 #include "backward.cuh"
 #include "common.cuh"
+#include "kv4.cuh"
 #include "sm100.cuh"
 
 using namespace msa;
@@ -1014,6 +1016,294 @@ msa_status msa_sparse_decode(const msa_bf16* q, const msa_bf16* q_idx, const msa
     a.block_idx_out = block_idx_out;
     a.err = (int*)workspace;
     return cuda_status(launch_decode(a, s), "decode launch");
+}
+
+// ------------------------------------------------------------------------------------ 4-bit cache
+static msa_status kv4_check(const msa_kv4_cache* c)
+{
+    if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || c->B < 1 || c->H_kv < 1 || c->d_h < 1 ||
+        c->L_max < 1)
+        return MSA_ERR_INVALID_ARG;
+    if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16) ||
+        !(c->k_scale > 0.f) || !(c->v_scale > 0.f) || std::isinf(c->k_scale) || std::isinf(c->v_scale))
+        return MSA_ERR_INVALID_ARG;
+    if (!(c->d_h == 64 || c->d_h == 128) || c->L_max % kBk != 0 || c->L_max > kMaxN || c->B > 65535 || c->H_kv > 65535)
+        return MSA_ERR_UNSUPPORTED;
+    // tiles of all sequences are counted in 32 bits, KV heads of all sequences are a grid dimension
+    if ((int64_t)c->B * c->H_kv > 65535 || (int64_t)c->B * c->H_kv * (c->L_max / 32) > 0x7FFFFFFF) return MSA_ERR_UNSUPPORTED;
+    return MSA_OK;
+}
+
+static int64_t kv4_rows(const msa_kv4_cache* c) { return (int64_t)c->B * c->H_kv * c->L_max; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) share anything.
+static bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + nb && y < x + na;
+}
+
+size_t msa_kv4_rows_workspace_size(void) { return kErrBytes; }
+
+static Kv4RowsArgs kv4_rows_args(const msa_kv4_cache* c, int64_t T, const int32_t* starts, const int32_t* cu, void* ws)
+{
+    Kv4RowsArgs a{};
+    a.codes[0] = c->k_codes;
+    a.codes[1] = c->v_codes;
+    a.scales[0] = c->k_scales;
+    a.scales[1] = c->v_scales;
+    a.t[0] = c->k_scale;
+    a.t[1] = c->v_scale;
+    a.starts = starts;
+    a.cu = cu;
+    a.T = T;
+    a.L_max = c->L_max;
+    a.B = c->B;
+    a.H_kv = c->H_kv;
+    a.d_h = c->d_h;
+    a.err = (int*)ws;
+    return a;
+}
+
+static msa_status kv4_rows_check(const msa_kv4_cache* c, const void* k, const void* v, int64_t T, const int32_t* starts,
+                                 const int32_t* cu, const void* workspace, size_t workspace_bytes)
+{
+    if (T < 0 || (T > 0 && (!k || !v)) || !starts || !workspace) return MSA_ERR_INVALID_ARG;
+    if (msa_status st = kv4_check(c)) return st;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(cu, 4) || !aligned(workspace, 256) ||
+        (!cu && T != c->B))
+        return MSA_ERR_INVALID_ARG;
+    if (T > kv4_rows(c)) return MSA_ERR_INVALID_ARG; // more rows than the cache has
+    if (workspace_bytes < kErrBytes) return MSA_ERR_WORKSPACE;
+    return MSA_OK;
+}
+
+msa_status msa_kv4_append(const msa_kv4_cache* cache, const msa_bf16* k, const msa_bf16* v, int64_t k_stride,
+                          int64_t v_stride, int64_t T, const int32_t* starts, const int32_t* cu_seqlens, void* workspace,
+                          size_t workspace_bytes, msa_stream_t stream)
+{
+    if (msa_status st = kv4_rows_check(cache, k, v, T, starts, cu_seqlens, workspace, workspace_bytes)) return st;
+    const int64_t row = (int64_t)cache->H_kv * cache->d_h;
+    if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0) return MSA_ERR_INVALID_ARG;
+    if (injected("msa_kv4_append")) return MSA_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
+    if (T == 0) return MSA_OK;
+    Kv4RowsArgs a = kv4_rows_args(cache, T, starts, cu_seqlens, workspace);
+    a.x[0] = k;
+    a.x[1] = v;
+    a.x_stride[0] = k_stride;
+    a.x_stride[1] = v_stride;
+    trace_begin(s);
+    const cudaError_t e = launch_kv4_append(a, s);
+    trace_end(s, MSA_KERNEL_KV4_APPEND);
+    return cuda_status(e, "kv4 append launch");
+}
+
+msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf16* v, int64_t T, const int32_t* starts,
+                        const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes, msa_stream_t stream)
+{
+    if (msa_status st = kv4_rows_check(cache, k, v, T, starts, cu_seqlens, workspace, workspace_bytes)) return st;
+    if (injected("msa_kv4_read")) return MSA_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
+    if (T == 0) return MSA_OK;
+    Kv4RowsArgs a = kv4_rows_args(cache, T, starts, cu_seqlens, workspace);
+    a.y[0] = k;
+    a.y[1] = v;
+    trace_begin(s);
+    const cudaError_t e = launch_kv4_read(a, s);
+    trace_end(s, MSA_KERNEL_KV4_READ);
+    return cuda_status(e, "kv4 read launch");
+}
+
+// Workspace of the attention: error word and arrival counters (cleared by every call), partials, and
+// an lse for the weights when the caller wants none.
+static size_t kv4_attn_head_bytes() { return kErrBytes + align_up(kKv4Ctas * sizeof(int), 256); }
+
+size_t msa_kv4_decode_workspace_size(int B, int H_q)
+{
+    if (B < 1 || H_q < 1) return 0;
+    return kv4_attn_head_bytes() + align_up((size_t)2 * kKv4Ctas * kKv4PartFloats * 4, 256) +
+           align_up((size_t)B * H_q * 4, 256);
+}
+
+static msa_status kv4_decode_check(const msa_kv4_cache* c, const void* q, const int32_t* lens, int H_q, const float* w_in,
+                                   const float* w_out, float decay, const void* out, const float* lse, const void* workspace)
+{
+    if (!q || !lens || !out || !workspace || H_q < 1) return MSA_ERR_INVALID_ARG;
+    if (msa_status st = kv4_check(c)) return st;
+    if (H_q % c->H_kv != 0 || !aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || !aligned(lse, 4) ||
+        !aligned(w_in, 4) || !aligned(w_out, 4) || !aligned(workspace, 256) || !std::isfinite(decay) || (w_in && !w_out))
+        return MSA_ERR_INVALID_ARG;
+    if (w_in != w_out && overlap(w_in, (size_t)kv4_rows(c) * 4, w_out, (size_t)kv4_rows(c) * 4)) return MSA_ERR_INVALID_ARG;
+    if (H_q / c->H_kv > 16) return MSA_ERR_UNSUPPORTED;
+    return MSA_OK;
+}
+
+// Validated arguments; ws: kv4 part of the workspace, whose head the caller has cleared.
+static msa_status kv4_decode_run(const msa_kv4_cache* c, const msa_bf16* q, const int32_t* lens, int H_q,
+                                 const int32_t* block_idx, int k, int min_len, const float* w_in, float* w_out, float decay,
+                                 msa_bf16* out, float* lse, uint8_t* ws, int* err, cudaStream_t s)
+{
+    Kv4DecodeArgs a{};
+    a.q = q;
+    a.k_codes = c->k_codes;
+    a.k_scales = c->k_scales;
+    a.v_codes = c->v_codes;
+    a.v_scales = c->v_scales;
+    a.k_scale = c->k_scale;
+    a.v_scale = c->v_scale;
+    a.lens = lens;
+    a.block_idx = block_idx;
+    a.B = c->B;
+    a.H_q = H_q;
+    a.H_kv = c->H_kv;
+    a.d_h = c->d_h;
+    a.k = k;
+    a.L_max = c->L_max;
+    a.min_len = min_len;
+    a.out = out;
+    a.arrived = (int*)(ws + kErrBytes);
+    a.parts = (float*)(ws + kv4_attn_head_bytes());
+    a.lse = lse;
+    if (w_out && !lse) a.lse = (float*)((uint8_t*)a.parts + align_up((size_t)2 * kKv4Ctas * kKv4PartFloats * 4, 256));
+    a.w_in = w_in;
+    a.w_out = w_out;
+    a.decay = decay;
+    a.err = err;
+    return cuda_status(launch_kv4_decode(a, s), "kv4 decode launch");
+}
+
+msa_status msa_kv4_decode(const msa_kv4_cache* cache, const msa_bf16* q, const int32_t* lens, int H_q,
+                          const int32_t* block_idx, int k, const float* w_in, float* w_out, float decay, msa_bf16* out,
+                          float* lse, void* workspace, size_t workspace_bytes, msa_stream_t stream)
+{
+    if (msa_status st = kv4_decode_check(cache, q, lens, H_q, w_in, w_out, decay, out, lse, workspace)) return st;
+    if (block_idx && (k < 1 || !aligned(block_idx, 4))) return MSA_ERR_INVALID_ARG;
+    if (block_idx && k > kMaxK) return MSA_ERR_UNSUPPORTED;
+    if (workspace_bytes < msa_kv4_decode_workspace_size(cache->B, H_q)) return MSA_ERR_WORKSPACE;
+    if (injected("msa_kv4_decode")) return MSA_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kv4_attn_head_bytes(), s), "clearing the error word"))
+        return st0;
+    return kv4_decode_run(cache, q, lens, H_q, block_idx, k, 0, w_in, w_out, decay, out, lse, (uint8_t*)workspace,
+                          (int*)workspace, s);
+}
+
+size_t msa_sparse_decode_kv4_workspace_size(int B, int64_t L_max, int H_q, int H_kv, int B_k, int k)
+{
+    if (B < 1 || L_max < 1 || H_q < 1 || H_kv < 1 || B_k < 1 || k < 1) return 0;
+    const int64_t nb_max = (L_max + B_k - 1) / B_k;
+    return msa_kv4_decode_workspace_size(B, H_q) + align_up((size_t)B * H_kv * nb_max * 4, 256) +
+           align_up((size_t)B * H_kv * k * 4, 256) + align_up((size_t)B * 4, 256) + align_up((size_t)(B + 1) * 8, 256);
+}
+
+msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_bf16* q, const msa_bf16* q_idx,
+                                 const msa_bf16* k_idx_cache, const int32_t* lens, int H_q, int d_idx, int B_k, int k,
+                                 const float* w_in, float* w_out, float decay, msa_bf16* out, float* lse,
+                                 int32_t* block_idx_out, void* workspace, size_t workspace_bytes, msa_stream_t stream)
+{
+    if (!q_idx || !k_idx_cache || d_idx < 1 || B_k < 1 || k < 1) return MSA_ERR_INVALID_ARG;
+    if (msa_status st = kv4_decode_check(cache, q, lens, H_q, w_in, w_out, decay, out, lse, workspace)) return st;
+    if (!aligned(q_idx, 16) || !aligned(k_idx_cache, 16) || !aligned(block_idx_out, 4)) return MSA_ERR_INVALID_ARG;
+    const int64_t lanes_per_pos = (int64_t)cache->H_kv * d_idx / 8;
+    if (B_k != kBk || k > kMaxK || !(d_idx == 32 || d_idx == 64 || d_idx == 128) || lanes_per_pos > 32 ||
+        !pow2((int)lanes_per_pos))
+        return MSA_ERR_UNSUPPORTED;
+    if (workspace_bytes < msa_sparse_decode_kv4_workspace_size(cache->B, cache->L_max, H_q, cache->H_kv, B_k, k))
+        return MSA_ERR_WORKSPACE;
+    if (injected("msa_sparse_decode_kv4")) return MSA_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    uint8_t* ws = (uint8_t*)workspace;
+    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kv4_attn_head_bytes(), s), "clearing the error word"))
+        return st0;
+    const int B = cache->B, H_kv = cache->H_kv;
+    size_t off = msa_kv4_decode_workspace_size(B, H_q);
+    DecodeArgs a{};
+    a.q_idx = q_idx;
+    a.k_idx_cache = k_idx_cache;
+    a.lens = lens;
+    a.B = B;
+    a.L_max = cache->L_max;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.d_h = cache->d_h;
+    a.d_idx = d_idx;
+    a.k = k;
+    a.pooled = (float*)(ws + off);
+    off += align_up((size_t)B * H_kv * (cache->L_max / kBk) * 4, 256);
+    a.sel = (int32_t*)(ws + off);
+    off += align_up((size_t)B * H_kv * k * 4, 256);
+    a.nsel = (int32_t*)(ws + off);
+    off += align_up((size_t)B * 4, 256);
+    a.blk_prefix = (int64_t*)(ws + off);
+    a.block_idx_out = block_idx_out;
+    a.err = (int*)workspace;
+    if (msa_status st = cuda_status(launch_decode_index(a, s), "decode index launch")) return st;
+    return kv4_decode_run(cache, q, lens, H_q, a.sel, k, 1, w_in, w_out, decay, out, lse, ws, (int*)workspace, s);
+}
+
+size_t msa_kv4_evict_workspace_size(int, int, int) { return kErrBytes; }
+
+msa_status msa_kv4_evict(const msa_kv4_cache* cache, const msa_kv4_cache* to, const float* w, const int32_t* lens, int keep,
+                         int recent, int first, const msa_bf16* k_idx, msa_bf16* k_idx_to, int d_idx, float* w_to,
+                         int32_t* lens_to, int32_t* kept, void* workspace, size_t workspace_bytes, msa_stream_t stream)
+{
+    if (!w || !lens || !lens_to || !kept || !workspace || keep < 1 || recent < 0 || first < 0 ||
+        (int64_t)recent + first > keep || !k_idx != !k_idx_to || (k_idx && d_idx < 1))
+        return MSA_ERR_INVALID_ARG;
+    if (msa_status st = kv4_check(cache)) return st;
+    if (msa_status st = kv4_check(to)) return st;
+    const int B = cache->B, H_kv = cache->H_kv, d_h = cache->d_h;
+    if (to->B != B || to->H_kv != H_kv || to->d_h != d_h || to->k_scale != cache->k_scale || to->v_scale != cache->v_scale ||
+        to->L_max < keep)
+        return MSA_ERR_INVALID_ARG;
+    if (!aligned(w, 4) || !aligned(w_to, 4) || !aligned(lens, 4) || !aligned(lens_to, 4) || !aligned(kept, 4) ||
+        !aligned(k_idx, 16) || !aligned(k_idx_to, 16) || !aligned(workspace, 256))
+        return MSA_ERR_INVALID_ARG;
+    if (k_idx && !(d_idx == 32 || d_idx == 64 || d_idx == 128)) return MSA_ERR_UNSUPPORTED;
+    const size_t n = (size_t)kv4_rows(cache), nt = (size_t)kv4_rows(to);
+    const struct { const void* p; size_t bytes; } src[] = {
+        {cache->k_codes, n * d_h / 2}, {cache->k_scales, n * d_h / 16}, {cache->v_codes, n * d_h / 2},
+        {cache->v_scales, n * d_h / 16}, {w, n * 4}, {k_idx, n * d_idx * 2}, {lens, (size_t)B * 4}},
+        dst[] = {{to->k_codes, nt * d_h / 2}, {to->k_scales, nt * d_h / 16}, {to->v_codes, nt * d_h / 2},
+                 {to->v_scales, nt * d_h / 16}, {w_to, nt * 4}, {k_idx_to, nt * d_idx * 2}, {lens_to, (size_t)B * 4},
+                 {kept, (size_t)B * H_kv * keep * 4}};
+    for (const auto& x : src)
+        for (const auto& y : dst)
+            if (overlap(x.p, x.bytes, y.p, y.bytes)) return MSA_ERR_INVALID_ARG;
+    if (workspace_bytes < msa_kv4_evict_workspace_size(B, H_kv, keep)) return MSA_ERR_WORKSPACE;
+    if (injected("msa_kv4_evict")) return MSA_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
+    Kv4EvictArgs a{};
+    a.k_codes = cache->k_codes;
+    a.k_scales = cache->k_scales;
+    a.v_codes = cache->v_codes;
+    a.v_scales = cache->v_scales;
+    a.k_codes_to = to->k_codes;
+    a.k_scales_to = to->k_scales;
+    a.v_codes_to = to->v_codes;
+    a.v_scales_to = to->v_scales;
+    a.k_idx = k_idx;
+    a.k_idx_to = k_idx_to;
+    a.w = w;
+    a.w_to = w_to;
+    a.lens = lens;
+    a.lens_to = lens_to;
+    a.kept = kept;
+    a.B = B;
+    a.H_kv = H_kv;
+    a.d_h = d_h;
+    a.d_idx = k_idx ? d_idx : 0;
+    a.keep = keep;
+    a.recent = recent;
+    a.first = first;
+    a.L_max = cache->L_max;
+    a.L_to = to->L_max;
+    a.err = (int*)workspace;
+    return cuda_status(launch_kv4_evict(a, s), "kv4 evict launch");
 }
 
 } // extern "C"

@@ -368,6 +368,116 @@ MSA_API msa_status msa_sparse_decode(const msa_bf16* q, const msa_bf16* q_idx, c
                              msa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
+ * 4-bit key/value cache: append, read, decode attention, eviction
+ *
+ * The pages name no 4-bit cache; this is the decode of [ABS] on a cache of 72 instead of 256 bytes
+ * per row of 128 elements. K and V rows are held as E2M1 codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6; bit 3 the sign; element 2i of a row in the low nibble of byte i, element 2i + 1 in the high
+ * one), one E4M3 scale per 16 consecutive elements and one fp32 scale t per tensor (k_scale,
+ * v_scale; 1 holds rows whose 16-element maxima lie between 0.1 and 2688 at full precision):
+ *   value = code * scale * t
+ *   y = fl32(x / t), a = max |y| of the 16, scale = E4M3(min(fl32(a / 6), 448)),
+ *   code = E2M1(fl32(y / scale)), zero codes where the scale rounds to 0
+ * with every rounding to nearest even and codes saturating at 6.
+ *
+ *   codes  : [B, H_kv, L_max, d_h / 2] uint8;  scales : [B, H_kv, L_max, d_h / 16] uint8 (E4M3)
+ * head-major, 16-byte aligned, caller-owned; rows never appended may hold anything. The struct is
+ * read on the host during the call. Supported: d_h in {64, 128}, L_max a multiple of 128 up to 2^21,
+ * H_q / H_kv any whole number up to 16, B * H_kv up to 65535, t positive and finite.
+ *
+ * Every call takes a workspace of at least the size its query returns (256-byte aligned; the device
+ * error word is at its start). Two calls that overlap in time need workspaces of their own. Captured
+ * calls may be replayed; the calls' device tensors (lens, starts, cu_seqlens) are read on replay.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales; /* device */
+    int32_t B, H_kv, d_h;
+    int64_t L_max;
+    float k_scale, v_scale;
+} msa_kv4_cache;
+
+/*
+ * msa_kv4_append: writes T new rows. cu_seqlens = NULL: T = B, row b goes to position starts[b] of
+ * sequence b (a decode step). Otherwise row i with cu_seqlens[b] <= i < cu_seqlens[b + 1] goes to
+ * position starts[b] + i - cu_seqlens[b] of sequence b (prompt chunks; empty sequences allowed).
+ *   k, v       : [T, H_kv, d_h] bf16, rows k_stride / v_stride elements apart (at least H_kv * d_h, a
+ *                multiple of 8: slices of a fused projection's output need no copy), 16-byte aligned
+ *   starts     : [B] int32 device;  cu_seqlens : [B + 1] int32 device, or NULL;  T >= 0
+ * Rows that the tables put outside the cache or outside [cu_seqlens[0], cu_seqlens[B]) are left out
+ * and reported (MSA_ERR_DEVICE_CHECK). No other row of the cache changes.
+ *
+ * msa_kv4_read: the same rows back, as bf16 values: k, v [T, H_kv, d_h], contiguous (rows left out as
+ * above are not written). What msa_sparse_prefill_varlen takes as cached prefixes.
+ */
+MSA_API size_t msa_kv4_rows_workspace_size(void);
+
+MSA_API msa_status msa_kv4_append(const msa_kv4_cache* cache, const msa_bf16* k, const msa_bf16* v, int64_t k_stride,
+                                  int64_t v_stride, int64_t T, const int32_t* starts, const int32_t* cu_seqlens,
+                                  void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+MSA_API msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf16* v, int64_t T, const int32_t* starts,
+                                const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes,
+                                msa_stream_t stream);
+
+/*
+ * msa_kv4_decode: one query token per sequence against the cache. Head h (KV head r = h / G) of
+ * sequence b attends to the positions j < lens[b] (block_idx = NULL), or to those of them in the
+ * blocks block_idx[b][r][0 .. k):
+ *   x_j = q[b,h] . K[b,r,j] / sqrt(d_h);  out = sum_j softmax(x)_j V[b,r,j];  lse = log sum_j exp(x_j)
+ * A row that sees no key (lens[b] = 0, or no block) gets out = 0 and lse = -inf.
+ * w_out != NULL also accumulates the attention weights of every visible position:
+ *   w_out[b][r][j] = decay * w_in[b][r][j] + sum over the G heads of softmax(x)_j     for j < lens[b]
+ * (the sum is 0 for positions outside the given blocks; w_in = NULL counts as 0; positions from
+ * lens[b] on are left as they were).
+ *   q, out    : [B, H_q, d_h] bf16, 16-byte aligned;  lse : [B, H_q] fp32, or NULL
+ *   lens      : [B] int32 device, 0 <= lens[b] <= L_max, else reported (MSA_ERR_DEVICE_CHECK) and the
+ *               sequence's outputs are left unwritten
+ *   block_idx : [B, H_kv, k] int32 device (1 <= k <= 16), ascending without repetition, -1 where there
+ *               is no block (as msa_sparse_decode gives them), or NULL; other entries are left out and
+ *               reported. B_k = 128
+ *   w_in, w_out : [B, H_kv, L_max] fp32, the same array or two that do not overlap
+ * Sums, softmax statistics and weights are fp32, P and the dequantised values (exact) fp16, out bf16.
+ *
+ * msa_sparse_decode_kv4: msa_sparse_decode (index scores, Top-k, attention over the selected blocks)
+ * with K and V in the 4-bit cache. Arguments as there (1 <= lens[b] <= L_max) and above.
+ */
+MSA_API size_t msa_kv4_decode_workspace_size(int B, int H_q);
+
+MSA_API msa_status msa_kv4_decode(const msa_kv4_cache* cache, const msa_bf16* q, const int32_t* lens, int H_q,
+                                  const int32_t* block_idx, int k, const float* w_in, float* w_out, float decay,
+                                  msa_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                                  msa_stream_t stream);
+
+MSA_API size_t msa_sparse_decode_kv4_workspace_size(int B, int64_t L_max, int H_q, int H_kv, int B_k, int k);
+
+MSA_API msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_bf16* q, const msa_bf16* q_idx,
+                                         const msa_bf16* k_idx_cache, const int32_t* lens, int H_q, int d_idx, int B_k,
+                                         int k, const float* w_in, float* w_out, float decay, msa_bf16* out, float* lse,
+                                         int32_t* block_idx_out, void* workspace, size_t workspace_bytes,
+                                         msa_stream_t stream);
+
+/*
+ * msa_kv4_evict: copies what is kept of every (sequence, KV head) to the front of another cache. Of n =
+ * lens[b] tokens all stay when n <= keep; otherwise the first `first`, the last `recent` and, of the
+ * others, those with the largest accumulated weight w[b][r][j] (equal weights: the lower position)
+ * stay, `keep` in all, in their order. KV heads keep different tokens; every one keeps the same number.
+ *   to       : the other cache: the same B, H_kv, d_h, k_scale and v_scale, L_max >= keep; no overlap
+ *   w        : [B, H_kv, cache->L_max] fp32;  w_to : [B, H_kv, to->L_max] fp32 out, or NULL
+ *   k_idx    : [B, cache->L_max, H_kv, d_idx] bf16 index keys, 16-byte aligned, or NULL (d_idx = 0, k_idx_to
+ *              = NULL);  k_idx_to : [B, to->L_max, H_kv, d_idx] out;  d_idx in {32, 64, 128}
+ *   lens     : [B] int32 device, 0 <= lens[b] <= cache->L_max (else reported and treated as empty)
+ *   lens_to  : [B] int32 device out = min(lens, keep);  kept : [B, H_kv, keep] int32 out, -1 padded
+ * 1 <= keep, 0 <= first, 0 <= recent, first + recent <= keep. Rows of `to` (and of w_to, k_idx_to) from
+ * lens_to[b] on are left as they were.
+ */
+MSA_API size_t msa_kv4_evict_workspace_size(int B, int H_kv, int keep);
+
+MSA_API msa_status msa_kv4_evict(const msa_kv4_cache* cache, const msa_kv4_cache* to, const float* w,
+                                 const int32_t* lens, int keep, int recent, int first, const msa_bf16* k_idx,
+                                 msa_bf16* k_idx_to, int d_idx, float* w_to, int32_t* lens_to, int32_t* kept,
+                                 void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
  * Tracing (measurement support; no counterpart on the pages)
  *
  * msa_trace_set() installs a caller-owned record: while installed, every entry point records
@@ -389,7 +499,12 @@ typedef enum {
     MSA_KERNEL_BWD_PREP = 9,    /* backward: rowsum(dout * out)                                 */
     MSA_KERNEL_BWD_ATTN = 10,   /* backward: KV-outer gradients                                 */
     MSA_KERNEL_BWD_CONVERT = 11, /* backward: fp32 accumulators to bf16                         */
-    MSA_KERNEL_QUANT = 12       /* E4M3 quantisation of one tensor                               */
+    MSA_KERNEL_QUANT = 12,      /* E4M3 quantisation of one tensor                               */
+    MSA_KERNEL_KV4_APPEND = 13, /* rows into the 4-bit cache                                     */
+    MSA_KERNEL_KV4_READ = 14,   /* rows of the 4-bit cache to bf16                               */
+    MSA_KERNEL_KV4_ATTN = 15,   /* single-token attention over the 4-bit cache                   */
+    MSA_KERNEL_KV4_WEIGHTS = 16, /* accumulated attention weights                                */
+    MSA_KERNEL_KV4_EVICT = 17   /* eviction: selection and row copies                            */
 } msa_kernel_id;
 
 typedef struct {
