@@ -5,12 +5,12 @@
 //   w_out[r][j] = decay * w_in[r][j] + sum over the heads of r of softmax(x)_j      (optional)
 //
 // Bound by reading the cache (d_h + d_h / 8 bytes per token and KV head). One CTA per SM walks an
-// equal contiguous slice of the flattened list of 32-key tiles of all (sequence, KV head) pairs, so
-// ragged batches and single long sequences load every SM alike. Inside a CTA every warp takes every
-// kWarps-th tile, streams it by bulk copies into a ring of its own (no CTA-wide synchronisation in
-// the loop) and keeps a running maximum, sum and output of its tiles; the warps' results are joined
-// at the end of each (sequence, KV head), and those of a pair that several CTAs share by the CTA
-// that finishes it last, in a fixed order (results do not depend on timing).
+// equal contiguous slice of the flattened list of 128-key blocks of all (sequence, KV head) pairs, so
+// ragged batches and single long sequences load every SM alike. Bulk copies bring kBlocks blocks at a
+// time into a ring of kStages such chunks; every warp takes 32 keys of a chunk and keeps a running
+// maximum, sum and output of its own, joined when the CTA leaves a (sequence, KV head). What several
+// CTAs hold of one pair is joined by the CTA that finishes last, in a fixed order (results do not
+// depend on timing).
 //
 // The heads of a KV head are the 16 rows of mma.sync m16n8k16 (a 16-row problem is below the 128-row
 // tcgen05 tile). E2M1 codes become fp16 pairs with the hardware conversion, times the E4M3 scale
@@ -32,125 +32,126 @@ namespace msa {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kBlocks = 3;          // blocks of a chunk
+constexpr int kStages = 3;          // chunks of the ring
+constexpr int kWarps = 4 * kBlocks; // a warp takes 32 keys of a chunk
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 32;  // keys of a tile
-constexpr int kStages = 4; // tiles in flight per warp
-constexpr int kTilesPerBlock = kBk / kTile;
-constexpr float kHeadroom = 7.f; // P's reference: log2 units below the maximum it was set from
-constexpr float kRaise = 15.f;   // P stays below 2^15, within fp16
+constexpr int kSlots = kWarps / 2; // join scratch: one output per pair of warps
+constexpr int kTile = 32;          // keys of a warp's part
+constexpr float kHeadroom = 7.f;   // P's reference: log2 units below the maximum it was set from
+constexpr float kRaise = 15.f;     // P stays below 2^15, within fp16
 
 template <int DH>
 struct Cfg {
     static constexpr int CODE = DH / 2, NG = DH / 16; // bytes of a row's codes, scales
-    static constexpr int K_CODES = 0, V_CODES = kTile * CODE, K_SCALES = 2 * kTile * CODE,
-                         V_SCALES = K_SCALES + kTile * NG, STAGE = V_SCALES + kTile * NG;
-    // join scratch: [warp][16 rows][4 lanes][DH / 4], padded so that 16-byte accesses do not conflict
+    static constexpr int KEYS = kBlocks * kBk;        // of a stage
+    static constexpr int K_CODES = 0, V_CODES = KEYS * CODE, K_SCALES = 2 * KEYS * CODE, V_SCALES = K_SCALES + KEYS * NG,
+                         STAGE = V_SCALES + KEYS * NG;
+    // join scratch: [slot][16 rows][4 lanes][DH / 4], padded so that 16-byte accesses do not conflict
     static constexpr int LANE = DH / 4 + 4, ROW = 4 * LANE, WARP = 16 * ROW;
-    static constexpr int SMEM = kWarps * kStages * STAGE + kWarps * WARP * 4;
+    // the join of several CTAs' partials uses the same memory: weights and sums [kKv4Ctas][16], thread groups' outputs
+    static constexpr int WARPS = kSlots * WARP, PARTS = kKv4Ctas * 32 + kThreads / 128 * 16 * DH;
+    static constexpr int SMEM = kStages * STAGE + (WARPS > PARTS ? WARPS : PARTS) * 4;
 };
 
 struct Shared {
-    uint64_t full[kWarps][kStages];
-    float m[kWarps][16], l[kWarps][16];
-    int warp_tiles[kWarps];
-    int b0, seg0;  // sequence holding the slice's first tile, first tile of that sequence
-    int last;      // this CTA joins the partials of the segment
+    uint64_t full[kStages], empty[kStages];
+    float m[kSlots][16], l[kSlots][16];
+    float part_l[16];
+    int warp_blocks[kWarps];
+    int b0, seg0; // sequence holding the slice's first block, first block of that sequence
+    int last;     // this CTA joins the partials of the segment
     int abort_flag;
 };
 
-// The flattened list: sequence b owns H_kv * tiles(b) tiles, KV head by KV head.
+// The flattened list: sequence b owns H_kv * blocks(b) blocks, KV head by KV head. With given blocks
+// every KV head has k, padding among them.
 struct Work {
     const Kv4DecodeArgs& a;
     __device__ __forceinline__ bool valid(int len) const { return len >= a.min_len && len <= a.L_max; }
-    __device__ __forceinline__ int tiles(int b) const // per KV head
+    __device__ __forceinline__ int blocks(int len) const // per KV head
     {
-        const int len = a.lens[b];
         if (!valid(len) || len == 0) return 0;
-        return a.block_idx ? a.k * kTilesPerBlock : (len + kTile - 1) / kTile;
+        return a.block_idx ? a.k : (len + kBk - 1) / kBk;
     }
-    // Tile `tile` of (b, r): its first key and how many of its keys are visible (0: nothing to read).
-    __device__ __forceinline__ int keys(int b, int r, int tile, int len, int& key0) const
+    // First key of entry i of (b, r); -1 for padding and for entries the check reports.
+    __device__ __forceinline__ int key0(int b, int r, int i, int len) const
     {
-        if (!a.block_idx) {
-            key0 = tile * kTile;
-            return min(kTile, len - key0);
-        }
-        const int slot = tile / kTilesPerBlock;
+        if (!a.block_idx) return i * kBk;
         const int32_t* sel = a.block_idx + ((int64_t)b * a.H_kv + r) * a.k;
-        const int blk = sel[slot];
-        if (blk < 0 || blk > (len - 1) / kBk || (slot > 0 && blk <= sel[slot - 1])) return 0; // padding, or reported by the check
-        key0 = blk * kBk + (tile % kTilesPerBlock) * kTile;
-        return max(0, min(kTile, len - key0));
+        const int blk = sel[i];
+        if (blk < 0 || blk > (len - 1) / kBk || (i > 0 && blk <= sel[i - 1])) return -1;
+        return blk * kBk;
     }
 };
 
-// Block-wide: number of tiles of all sequences, and for the caller's slice its first sequence.
-// Sequences are split among the threads in contiguous runs.
-__device__ __forceinline__ int64_t total_tiles(const Work& w, Shared& sh, int64_t& before, int& b_lo, int& b_hi)
+// Block-wide: the number of blocks of all sequences (below 2^31, checked on the host for full caches).
+// Sequences [b_lo, b_hi) are the calling thread's, `before` the blocks of those before them.
+template <int THREADS>
+__device__ __forceinline__ int total_blocks(const Work& w, int* warp_blocks, int& before, int& b_lo, int& b_hi)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (w.a.B + kThreads - 1) / kThreads;
+    const int per = (w.a.B + THREADS - 1) / THREADS;
     b_lo = min(w.a.B, tid * per);
     b_hi = min(w.a.B, b_lo + per);
     int n = 0;
-    for (int b = b_lo; b < b_hi; ++b) n += w.tiles(b) * w.a.H_kv;
+    for (int b = b_lo; b < b_hi; ++b) n += w.blocks(w.a.lens[b]) * w.a.H_kv;
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) sh.warp_tiles[warp] = x;
+    if (lane == 31) warp_blocks[warp] = x;
     __syncthreads();
-    int64_t total = 0;
+    int total = 0;
     before = x - n;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const int y = sh.warp_tiles[i];
+    for (int i = 0; i < THREADS / 32; ++i) {
+        const int y = warp_blocks[i];
         if (i < warp) before += y;
         total += y;
     }
     return total;
 }
 
-// A warp's walk over its tiles of the CTA's slice [lo, hi): segment by segment (a segment is a
-// (sequence, KV head)), every kWarps-th tile of the part of it that lies in the slice.
+// A walk over the slice [lo, hi), segment by segment (a segment is a (sequence, KV head)).
 struct Walk {
-    int b, r, n;       // sequence, KV head, tiles of a segment of this sequence
-    int64_t seg;       // first tile of the segment
-    int64_t lo, hi;    // the slice
-    int64_t tile, end; // next tile of this warp, end of the segment's part
-    int len;
+    int b, r, len, n; // sequence, KV head, length, blocks of a segment of this sequence
+    int seg;          // first block of the segment
+    int lo, hi;       // the slice
+    int pos, end;     // the part of the segment in the slice, from the next block on
 
-    __device__ __forceinline__ void enter(int warp)
+    __device__ __forceinline__ void enter()
     {
-        tile = (seg > lo ? seg : lo) + warp;
-        end = seg + n < hi ? seg + n : hi;
+        pos = max(seg, lo);
+        end = min(seg + n, hi);
     }
-    __device__ __forceinline__ void begin(const Work& w, int b0, int64_t seq0, int64_t lo_, int64_t hi_, int warp)
+    __device__ __forceinline__ void begin(const Work& w, int b0, int seq0, int lo_, int hi_)
     {
         lo = lo_;
         hi = hi_;
         b = b0;
-        n = w.tiles(b);
         len = w.a.lens[b];
-        r = (int)((lo - seq0) / n);
-        seg = seq0 + (int64_t)r * n;
-        enter(warp);
+        n = w.blocks(len);
+        r = (lo - seq0) / n;
+        seg = seq0 + r * n;
+        enter();
     }
     __device__ __forceinline__ bool more() const { return seg < hi; }
-    __device__ __forceinline__ void next_segment(const Work& w, int warp)
+    __device__ __forceinline__ void next_segment(const Work& w)
     {
         seg += n;
         if (++r == w.a.H_kv) {
             r = 0;
             if (seg < hi) {
-                do { ++b; } while ((n = w.tiles(b)) == 0);
-                len = w.a.lens[b];
+                do {
+                    len = w.a.lens[++b];
+                    n = w.blocks(len);
+                } while (n == 0);
             }
         }
-        enter(warp);
+        enter();
     }
 };
 
@@ -193,31 +194,37 @@ template <int DH>
 __device__ __forceinline__ void scores(const uint8_t* kc, const uint8_t* ks, const uint32_t (&qf)[DH / 16][4], int g, int t,
                                        float (&x)[4][4])
 {
+    uint32_t c[4][DH / 32], s[4][DH / 64];
+    const int row = (g >> 1) + 4 * (g & 1);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-        const int key = 8 * n + (g >> 1) + 4 * (g & 1);
-        uint32_t c[DH / 32], s[2];
+        const int key = 8 * n + row;
         if constexpr (DH == 128) {
             const uint4 v = *reinterpret_cast<const uint4*>(kc + key * 64 + t * 16);
-            c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+            c[n][0] = v.x, c[n][1] = v.y, c[n][2] = v.z, c[n][3] = v.w;
             const uint32_t sc = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + key * 8 + t * 2));
-            s[0] = prmt(sc, sc, 0x1010);
-            s[1] = prmt(sc, sc, 0x3232);
+            s[n][0] = prmt(sc, sc, 0x1010);
+            s[n][1] = prmt(sc, sc, 0x3232);
         } else {
             const uint2 v = *reinterpret_cast<const uint2*>(kc + key * 32 + t * 8);
-            c[0] = v.x, c[1] = v.y;
+            c[n][0] = v.x, c[n][1] = v.y;
             const uint32_t sc = e4m3x2_to_f16x2(ks[key * 4 + t]);
-            s[0] = prmt(sc, sc, 0x1010);
+            s[n][0] = prmt(sc, sc, 0x1010);
         }
 #pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
-            uint32_t h[4];
-            e2m1x8_to_f16x2(c[i], h);
-            mma_f16_16816(x[n], qf[2 * i], mul_f16x2(h[0], s[i / 2]), mul_f16x2(h[1], s[i / 2]));
-            mma_f16_16816(x[n], qf[2 * i + 1], mul_f16x2(h[2], s[i / 2]), mul_f16x2(h[3], s[i / 2]));
+        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < DH / 32; ++i) {
+        uint32_t h[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            e2m1x8_to_f16x2(c[n][i], h[n]);
+            mma_f16_16816(x[n], qf[2 * i], mul_f16x2(h[n][0], s[n][i / 2]), mul_f16x2(h[n][1], s[n][i / 2]));
         }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            mma_f16_16816(x[n], qf[2 * i + 1], mul_f16x2(h[n][2], s[n][i / 2]), mul_f16x2(h[n][3], s[n][i / 2]));
     }
 }
 
@@ -237,27 +244,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
     using C = Cfg<DH>;
     constexpr int KS = DH / 16; // contraction steps of S
     constexpr int NT = DH / 8;  // output tiles of O
-    extern __shared__ __align__(128) uint8_t ring_smem[];
+    extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
-    float* join = reinterpret_cast<float*>(ring_smem + kWarps * kStages * C::STAGE);
+    float* join = reinterpret_cast<float*>(ring + kStages * C::STAGE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.H_q / a.H_kv;
     const Work w{a};
 
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[warp][i], 1);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kWarps);
+        }
         fence_mbar_init();
+        sh.abort_flag = 0;
     }
-    if (tid == 0) sh.abort_flag = 0;
-    int64_t before;
-    int b_lo, b_hi;
-    const int64_t total = total_tiles(w, sh, before, b_lo, b_hi);
-    // every CTA gets at least one tile per warp where there are that many
-    int64_t n_cta = (total + kWarps - 1) / kWarps;
-    n_cta = n_cta < gridDim.x ? n_cta : gridDim.x;
+    int before, b_lo, b_hi;
+    const int total = total_blocks<kThreads>(w, sh.warp_blocks, before, b_lo, b_hi);
+    const int n_cta = min((total + kBlocks - 1) / kBlocks, (int)gridDim.x); // a chunk for every CTA where there are that many
     const int cta = blockIdx.x;
-    // sequences without keys (and rejected ones) have no tiles: CTA 0 answers for them
-    if (cta == 0) {
+    // sequences without keys have no blocks: the last CTA answers for them, and reports what is rejected
+    if (cta == (int)gridDim.x - 1) {
         for (int b = warp; b < a.B; b += kWarps) {
             const int len = a.lens[b];
             if (!w.valid(len)) {
@@ -269,60 +276,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                     for (int e = lane; e < a.H_q; e += 32) a.lse[(int64_t)b * a.H_q + e] = -CUDART_INF_F;
             } else if (a.block_idx) {
                 for (int e = lane; e < a.H_kv * a.k; e += 32) {
-                    const int32_t* sel = a.block_idx + (int64_t)b * a.H_kv * a.k + e;
-                    const bool ok = *sel >= -1 && *sel <= (len - 1) / kBk && (e % a.k == 0 || *sel < 0 || sel[-1] < *sel);
-                    if (!ok) report_error(a.err, MSA_ERR_DEVICE_CHECK, 210);
+                    const int r = e / a.k, i = e % a.k;
+                    if (w.key0(b, r, i, len) < 0 && a.block_idx[(int64_t)b * a.H_kv * a.k + e] != -1)
+                        report_error(a.err, MSA_ERR_DEVICE_CHECK, 210);
                 }
             }
         }
     }
     if (cta >= n_cta) return;
-    const int64_t lo = total * cta / n_cta, hi = total * (cta + 1) / n_cta;
+    const int lo = (int)((int64_t)total * cta / n_cta), hi = (int)((int64_t)total * (cta + 1) / n_cta);
     for (int b = b_lo; b < b_hi; ++b) {
-        const int64_t n = (int64_t)w.tiles(b) * a.H_kv;
+        const int n = w.blocks(a.lens[b]) * a.H_kv;
         if (lo >= before && lo < before + n) {
             sh.b0 = b;
-            sh.seg0 = (int)before;
+            sh.seg0 = before;
         }
         before += n;
     }
     __syncthreads();
 
-    uint8_t* ring = ring_smem + warp * kStages * C::STAGE;
-    uint64_t* full = sh.full[warp];
     volatile int* abort_flag = &sh.abort_flag;
     Walk prod, cons;
-    cons.begin(w, sh.b0, sh.seg0, lo, hi, warp);
+    cons.begin(w, sh.b0, sh.seg0, lo, hi);
     prod = cons;
-    int64_t issued = 0, used = 0;
-    // Starts the copies of the warp's next tile that has visible keys; false when there is none.
-    auto issue = [&]() {
-        while (prod.more()) {
-            while (prod.tile < prod.end) {
-                int key0;
-                const int nk = w.keys(prod.b, prod.r, (int)(prod.tile - prod.seg), prod.len, key0);
-                prod.tile += kWarps;
-                if (nk == 0) continue;
-                if (lane == 0) {
-                    uint8_t* st = ring + (issued % kStages) * C::STAGE;
-                    uint64_t* bar = &full[issued % kStages];
-                    const int64_t row = ((int64_t)prod.b * a.H_kv + prod.r) * a.L_max + key0; // L_max is whole blocks
-                    mbar_arrive_expect_tx(bar, C::STAGE);
-                    bulk_load(st + C::K_CODES, a.k_codes + row * C::CODE, kTile * C::CODE, bar);
-                    bulk_load(st + C::K_SCALES, a.k_scales + row * C::NG, kTile * C::NG, bar);
-                    bulk_load(st + C::V_CODES, a.v_codes + row * C::CODE, kTile * C::CODE, bar);
-                    bulk_load(st + C::V_SCALES, a.v_scales + row * C::NG, kTile * C::NG, bar);
-                }
-                ++issued;
-                return;
+    uint32_t issued = 0, used = 0; // chunks
+    // Lane 0 of warp 0 starts the copies of the next chunk: up to kBlocks blocks of one segment, the
+    // visible rows rounded up to 32 (L_max is whole blocks).
+    auto issue = [&] {
+        if (!prod.more()) return true;
+        const uint32_t st = issued % kStages, round = issued / kStages;
+        if (round > 0 && !wait_or_abort(&sh.empty[st], (round - 1) & 1, abort_flag, a.err, 62, kWaitLimit)) return false;
+        uint8_t* s = ring + st * C::STAGE;
+        const int64_t row0 = ((int64_t)prod.b * a.H_kv + prod.r) * a.L_max;
+        const int nb = min(kBlocks, prod.end - prod.pos);
+        auto copy = [&](int key, int at, int rows) {
+            bulk_load(s + C::K_CODES + at * C::CODE, a.k_codes + (row0 + key) * C::CODE, rows * C::CODE, &sh.full[st]);
+            bulk_load(s + C::K_SCALES + at * C::NG, a.k_scales + (row0 + key) * C::NG, rows * C::NG, &sh.full[st]);
+            bulk_load(s + C::V_CODES + at * C::CODE, a.v_codes + (row0 + key) * C::CODE, rows * C::CODE, &sh.full[st]);
+            bulk_load(s + C::V_SCALES + at * C::NG, a.v_scales + (row0 + key) * C::NG, rows * C::NG, &sh.full[st]);
+        };
+        if (!a.block_idx) {
+            const int key = (prod.pos - prod.seg) * kBk;
+            const int rows = min(nb * kBk, (prod.len - key + kTile - 1) / kTile * kTile);
+            mbar_arrive_expect_tx(&sh.full[st], rows * 2 * (C::CODE + C::NG));
+            copy(key, 0, rows);
+        } else {
+            int key[kBlocks], rows[kBlocks], all = 0;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                key[i] = i < nb ? w.key0(prod.b, prod.r, prod.pos - prod.seg + i, prod.len) : -1;
+                rows[i] = key[i] < 0 ? 0 : min(kBk, (prod.len - key[i] + kTile - 1) / kTile * kTile);
+                all += rows[i];
             }
-            prod.next_segment(w, warp);
+            mbar_arrive_expect_tx(&sh.full[st], all * 2 * (C::CODE + C::NG));
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
+                if (rows[i] > 0) copy(key[i], i * kBk, rows[i]);
         }
+        ++issued;
+        prod.pos += nb;
+        if (prod.pos >= prod.end) prod.next_segment(w);
+        return true;
     };
-    for (int i = 0; i < kStages; ++i) issue();
-
     bool ok = true;
-    for (; cons.more(); cons.next_segment(w, warp)) {
+    if (tid == 0)
+        for (int i = 0; i < kStages - 1; ++i) ok = issue() && ok;
+
+    for (; cons.more(); cons.next_segment(w)) {
         uint32_t qf[KS][4];
         float f0, f1;
         load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
@@ -333,36 +353,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
         float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f; // references, this lane's sums
 
-        for (; ok && cons.tile < cons.end; cons.tile += kWarps) {
-            int key0;
-            const int nk = w.keys(cons.b, cons.r, (int)(cons.tile - cons.seg), cons.len, key0);
-            if (nk == 0) continue;
-            const int st = (int)(used % kStages);
-            ok = wait_or_abort(&full[st], (uint32_t)((used / kStages) & 1), abort_flag, a.err, 60, kWaitLimit);
+        for (; ok && cons.pos < cons.end; cons.pos += kBlocks, ++used) {
+            if (tid == 0) ok = issue();
+            const uint32_t st = used % kStages;
+            ok = ok && wait_or_abort(&sh.full[st], (used / kStages) & 1, abort_flag, a.err, 60, kWaitLimit);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            ++used;
+            int nk = 0; // visible keys of the warp's 32
+            if (cons.pos + warp / 4 < cons.end) {
+                const int key = w.key0(cons.b, cons.r, cons.pos + warp / 4 - cons.seg, cons.len);
+                if (key >= 0) nk = min(kTile, cons.len - key - kTile * (warp & 3));
+            }
+            if (nk <= 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.empty[st]);
+                continue;
+            }
             const uint8_t* s = ring + st * C::STAGE;
-            // ------------------------------------------------------------ S = Q K^T
             float x[4][4];
-            scores<DH>(s + C::K_CODES, s + C::K_SCALES, qf, g, t, x);
+            scores<DH>(s + C::K_CODES + warp * kTile * C::CODE, s + C::K_SCALES + warp * kTile * C::NG, qf, g, t, x);
+            const uint8_t* vc = s + C::V_CODES + warp * kTile * C::CODE;
+            uint8_t* vs = ring + st * C::STAGE + C::V_SCALES + warp * kTile * C::NG;
             // ------------------------------------------------------------ softmax
-            float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+            if (nk < kTile) { // the last tile of a segment
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool seen = 8 * n + t + 4 * e < nk;
-                    x[n][e] = seen ? x[n][e] * f0 : -CUDART_INF_F;
-                    x[n][2 + e] = seen ? x[n][2 + e] * f1 : -CUDART_INF_F;
-                    mx0 = fmaxf(mx0, x[n][e]);
-                    mx1 = fmaxf(mx1, x[n][2 + e]);
-                }
+                    for (int e = 0; e < 2; ++e)
+                        if (8 * n + t + 4 * e >= nk) x[n][e] = x[n][2 + e] = -CUDART_INF_F;
+                // rows past the length hold anything, NaN scales among it: they weigh 0 and must be finite
+                if (lane >= nk)
+                    for (int i = 0; i < C::NG; i += 4) *reinterpret_cast<uint32_t*>(vs + lane * C::NG + i) = 0u;
+                __syncwarp();
+                fence_proxy_async(); // the stage is written by a bulk copy again
+            }
+            float mx0 = max3f(x[0][0], x[0][1], x[1][0]), mx1 = max3f(x[0][2], x[0][3], x[1][2]);
+            mx0 = max3f(mx0, x[1][1], x[2][0]);
+            mx1 = max3f(mx1, x[1][3], x[2][2]);
+            mx0 = max3f(mx0, x[2][1], x[3][0]);
+            mx1 = max3f(mx1, x[2][3], x[3][2]);
+            mx0 = fmaxf(mx0, x[3][1]);
+            mx1 = fmaxf(mx1, x[3][3]);
 #pragma unroll
             for (int d = 1; d < 4; d <<= 1) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
             }
+            mx0 *= f0; // f > 0
+            mx1 *= f1;
             // the references move up only when P would leave [0, 2^15): exact, and rare
             if (__any_sync(0xffffffffu, mx0 > m0 + kRaise || mx1 > m1 + kRaise)) {
                 const float n0 = mx0 > m0 + kRaise ? mx0 - kHeadroom : m0, n1 = mx1 > m1 + kRaise ? mx1 - kHeadroom : m1;
@@ -382,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             uint32_t pf[2][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const float p0 = ex2_approx(x[n][0] - m0), p1 = ex2_approx(x[n][1] - m0);
-                const float p2 = ex2_approx(x[n][2] - m1), p3 = ex2_approx(x[n][3] - m1);
+                const float p0 = ex2_approx(fmaf(x[n][0], f0, -m0)), p1 = ex2_approx(fmaf(x[n][1], f0, -m0));
+                const float p2 = ex2_approx(fmaf(x[n][2], f1, -m1)), p3 = ex2_approx(fmaf(x[n][3], f1, -m1));
                 l0 += p0 + p1;
                 l1 += p2 + p3;
                 pf[n >> 1][(n & 1) * 2] = pack_f16x2(p0, p1);
@@ -397,21 +435,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                 for (int u = 0; u < 4; ++u) {
                     const int key = 16 * j + t + 4 * u;
                     if constexpr (DH == 128) {
-                        const uint2 c = *reinterpret_cast<const uint2*>(s + C::V_CODES + key * 64 + g * 8);
+                        const uint2 c = *reinterpret_cast<const uint2*>(vc + key * 64 + g * 8);
                         wv[u][0] = c.x;
                         wv[u][1] = c.y;
                     } else {
-                        wv[u][0] = *reinterpret_cast<const uint32_t*>(s + C::V_CODES + key * 32 + g * 4);
+                        wv[u][0] = *reinterpret_cast<const uint32_t*>(vc + key * 32 + g * 4);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int key = 16 * j + t + 8 * u;
                     const int gs = DH == 128 ? g : g >> 1;
-                    uint32_t sa = s[C::V_SCALES + key * C::NG + gs], sb = s[C::V_SCALES + (key + 4) * C::NG + gs];
-                    // rows past the length hold anything, NaN scales among it: they weigh 0 and must be finite
-                    if (key >= nk) sa = 0u;
-                    if (key + 4 >= nk) sb = 0u;
+                    const uint32_t sa = vs[key * C::NG + gs], sb = vs[(key + 4) * C::NG + gs];
                     sc[u] = e4m3x2_to_f16x2(sa | (sb << 8));
                 }
 #pragma unroll
@@ -428,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                 }
             }
             __syncwarp(); // every lane has read the stage
-            issue();
+            if (lane == 0) mbar_arrive(&sh.empty[st]);
         }
         // ------------------------------------------------------------ join the warps
 #pragma unroll
@@ -436,21 +471,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             l0 += __shfl_xor_sync(0xffffffffu, l0, d);
             l1 += __shfl_xor_sync(0xffffffffu, l1, d);
         }
-        if (t == 0) {
-            sh.m[warp][g] = m0;
-            sh.m[warp][g + 8] = m1;
-            sh.l[warp][g] = l0;
-            sh.l[warp][g + 8] = l1;
+        // two steps: the upper half of the warps hand theirs to the lower half
+        float* mine = join + (warp % kSlots) * C::WARP + t * C::LANE;
+        auto put = [&] {
+            if (t == 0) {
+                sh.m[warp % kSlots][g] = m0;
+                sh.m[warp % kSlots][g + 8] = m1;
+                sh.l[warp % kSlots][g] = l0;
+                sh.l[warp % kSlots][g + 8] = l1;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) // row g + 8 half: elements t * DH / 4 + (0 .. DH / 4)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 4)
+                        *reinterpret_cast<float4*>(mine + (g + 8 * half) * C::ROW + c * NT + n) = make_float4(
+                            o[n][2 * half + c], o[n + 1][2 * half + c], o[n + 2][2 * half + c], o[n + 3][2 * half + c]);
+        };
+        if (warp >= kSlots) put();
+        __syncthreads();
+        if (warp < kSlots) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float &m = half ? m1 : m0, &l = half ? l1 : l0;
+                const float om = sh.m[warp][g + 8 * half], M = fmaxf(m, om);
+                const float wa = join_weight(m, M), wb = join_weight(om, M);
+                l = fmaf(wa, l, wb * sh.l[warp][g + 8 * half]);
+                m = M;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(mine + (g + 8 * half) * C::ROW + c * NT + n);
+                        o[n][2 * half + c] = fmaf(wa, o[n][2 * half + c], wb * v.x);
+                        o[n + 1][2 * half + c] = fmaf(wa, o[n + 1][2 * half + c], wb * v.y);
+                        o[n + 2][2 * half + c] = fmaf(wa, o[n + 2][2 * half + c], wb * v.z);
+                        o[n + 3][2 * half + c] = fmaf(wa, o[n + 3][2 * half + c], wb * v.w);
+                    }
+            }
+            __syncwarp(); // every lane has read the rows' maxima and sums
+            put();
         }
-        float* mine = join + warp * C::WARP + t * C::LANE;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) // row g + 8 half: elements t * DH / 4 + (0 .. DH / 4)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int n = 0; n < NT; n += 4)
-                    *reinterpret_cast<float4*>(mine + (g + 8 * half) * C::ROW + c * NT + n) =
-                        make_float4(o[n][2 * half + c], o[n + 1][2 * half + c], o[n + 2][2 * half + c], o[n + 3][2 * half + c]);
         __syncthreads();
         const bool whole = cons.seg >= lo && cons.seg + cons.n <= hi; // no other CTA has tiles of it
         float* part = a.parts + (int64_t)(2 * cta + (cons.seg > lo ? 1 : 0)) * kKv4PartFloats;
@@ -458,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             const int row = e / (DH / 4), q4 = e % (DH / 4); // 4 elements at 4 * q4
             float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sh.m[i][row]);
+            for (int i = 0; i < kSlots; ++i) M = fmaxf(M, sh.m[i][row]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             const float* src = join + row * C::ROW + (q4 / (DH / 16)) * C::LANE + (q4 % (DH / 16)) * 4;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
+            for (int i = 0; i < kSlots; ++i) {
                 const float c = join_weight(sh.m[i][row], M);
                 const float4 v = *reinterpret_cast<const float4*>(src + i * C::WARP);
                 L = fmaf(c, sh.l[i][row], L);
@@ -485,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
         }
         if (!whole) {
             // the CTAs with tiles of this segment: that of its first tile .. that of its last
-            const int c0 = (int)(((cons.seg + 1) * n_cta - 1) / total), c1 = (int)(((cons.seg + cons.n) * n_cta - 1) / total);
+            const int c0 = (int)(((int64_t)(cons.seg + 1) * n_cta - 1) / total);
+            const int c1 = (int)(((int64_t)(cons.seg + cons.n) * n_cta - 1) / total);
             __threadfence();
             __syncthreads();
             if (tid == 0) sh.last = atomicAdd(&a.arrived[c0], 1) == c1 - c0;
@@ -493,75 +556,118 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             if (sh.last) {
                 __threadfence();
                 const int np = c1 - c0 + 1;
-                const int64_t lo0 = total * c0 / n_cta;
+                const int lo0 = (int)((int64_t)total * c0 / n_cta);
                 // slot of CTA c: the segment is its slice's first unless the slice starts before it (only c0's can)
-                auto slot = [&](int c) { return a.parts + (int64_t)(2 * c + (c == c0 && cons.seg > lo0 ? 1 : 0)) * kKv4PartFloats; };
-                for (int e = tid; e < G * (DH / 4); e += kThreads) {
-                    const int row = e / (DH / 4), q4 = e % (DH / 4);
+                const float* parts = a.parts + (int64_t)2 * c0 * kKv4PartFloats;
+                const int first = cons.seg > lo0 ? 1 : 0;
+                auto slot = [&](int c) { return parts + (int64_t)(c == 0 ? first : 2 * c) * kKv4PartFloats; };
+                float *cw = join, *cl = join + kKv4Ctas * 16, *sums = join + kKv4Ctas * 32;
+                for (int e = tid; e < np * 16; e += kThreads) {
+                    const int row = e % 16, c = e / 16;
+                    cw[c * 16 + row] = row < G ? __ldcg(slot(c) + 16 * 128 + row) : -CUDART_INF_F;
+                    cl[c * 16 + row] = row < G ? __ldcg(slot(c) + 16 * 128 + 16 + row) : 0.f;
+                }
+                __syncthreads();
+                for (int row = warp; row < G; row += kWarps) {
                     float M = -CUDART_INF_F, L = 0.f;
-                    for (int c = 0; c < np; ++c) M = fmaxf(M, __ldcg(slot(c0 + c) + 16 * 128 + row));
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = 0; c < np; ++c) {
-                        const float* p = slot(c0 + c);
-                        const float cw = join_weight(__ldcg(p + 16 * 128 + row), M);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + row * DH + q4 * 4));
-                        L = fmaf(cw, __ldcg(p + 16 * 128 + 16 + row), L);
-                        acc.x = fmaf(cw, v.x, acc.x);
-                        acc.y = fmaf(cw, v.y, acc.y);
-                        acc.z = fmaf(cw, v.z, acc.z);
-                        acc.w = fmaf(cw, v.w, acc.w);
+                    for (int c = lane; c < np; c += 32) M = fmaxf(M, cw[c * 16 + row]);
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                    for (int c = lane; c < np; c += 32) {
+                        const float wt = join_weight(cw[c * 16 + row], M);
+                        cw[c * 16 + row] = wt;
+                        L = fmaf(wt, cl[c * 16 + row], L);
                     }
-                    const int64_t orow = (int64_t)cons.b * a.H_q + cons.r * G + row;
-                    store_out(a, orow, q4 * 4, acc, L > 0.f ? a.v_scale / L : 0.f);
-                    if (a.lse && q4 == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -CUDART_INF_F;
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+                    if (lane == 0) {
+                        sh.part_l[row] = L > 0.f ? a.v_scale / L : 0.f;
+                        if (a.lse)
+                            a.lse[(int64_t)cons.b * a.H_q + cons.r * G + row] =
+                                L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -CUDART_INF_F;
+                    }
+                }
+                __syncthreads();
+                // groups of threads take every (number of groups)-th partial, each thread up to 4 x 4 elements
+                const int n4 = G * (DH / 4), width = n4 >= 128 ? 128 : (n4 >= 64 ? 64 : 32), groups = kThreads / width;
+                const int grp = tid / width, e0 = tid % width;
+                float4 acc[4] = {};
+#pragma unroll 4
+                for (int c = grp; c < np; c += groups) {
+                    const float* p = slot(c);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int e = e0 + u * width;
+                        if (e < n4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
+                            const float wt = cw[c * 16 + e / (DH / 4)];
+                            acc[u].x = fmaf(wt, v.x, acc[u].x);
+                            acc[u].y = fmaf(wt, v.y, acc[u].y);
+                            acc[u].z = fmaf(wt, v.z, acc[u].z);
+                            acc[u].w = fmaf(wt, v.w, acc[u].w);
+                        }
+                    }
+                }
+                float4* s4 = reinterpret_cast<float4*>(sums);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (e0 + u * width < n4) s4[grp * n4 + e0 + u * width] = acc[u];
+                __syncthreads();
+                for (int e = tid; e < n4; e += kThreads) {
+                    float4 v = s4[e];
+                    for (int i = 1; i < groups; ++i) {
+                        const float4 y = s4[i * n4 + e];
+                        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                    }
+                    const int row = e / (DH / 4);
+                    store_out(a, (int64_t)cons.b * a.H_q + cons.r * G + row, e % (DH / 4) * 4, v, sh.part_l[row]);
                 }
             }
         }
         __syncthreads(); // the join scratch is free again
     }
     // after an abort, copies may still be in flight: the shared memory must outlive them
-    if (!ok && lane == 0)
-        for (; used < issued; ++used) drain_wait(&full[used % kStages], (uint32_t)((used / kStages) & 1), a.err, 61, kWaitLimit);
+    if (tid == 0)
+        for (; used < issued; ++used) drain_wait(&sh.full[used % kStages], (used / kStages) & 1, a.err, 61, kWaitLimit);
 }
 
 // Accumulated weights, after the attention (they need the final lse): K is read once more, and every
-// visible key of the list gets its group's sum of softmax weights.
+// visible key of the list gets its group's sum of softmax weights. A warp takes 32 keys at a time.
+constexpr int kWThreads = 256;
+
 template <int DH>
-__global__ void __launch_bounds__(kThreads) kv4_weights_kernel(Kv4DecodeArgs a)
+__global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs a)
 {
     using C = Cfg<DH>;
-    __shared__ Shared sh;
+    __shared__ int warp_blocks[kWThreads / 32], b0, seg0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.H_q / a.H_kv;
     const Work w{a};
-    int64_t before;
-    int b_lo, b_hi;
-    const int64_t total = total_tiles(w, sh, before, b_lo, b_hi);
-    const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    int before, b_lo, b_hi;
+    const int total = total_blocks<kWThreads>(w, warp_blocks, before, b_lo, b_hi);
+    const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
     if (lo >= hi) return;
     for (int b = b_lo; b < b_hi; ++b) {
-        const int64_t n = (int64_t)w.tiles(b) * a.H_kv;
+        const int n = w.blocks(a.lens[b]) * a.H_kv;
         if (lo >= before && lo < before + n) {
-            sh.b0 = b;
-            sh.seg0 = (int)before;
+            b0 = b;
+            seg0 = before;
         }
         before += n;
     }
     __syncthreads();
     Walk cons;
-    for (cons.begin(w, sh.b0, sh.seg0, lo, hi, warp); cons.more(); cons.next_segment(w, warp)) {
-        if (cons.tile >= cons.end) continue;
+    for (cons.begin(w, b0, seg0, lo, hi); cons.more(); cons.next_segment(w)) {
         uint32_t qf[DH / 16][4];
         float f0, f1;
         load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
         const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
         const float z0 = g < G ? lse[g] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
         const float z1 = g + 8 < G ? lse[g + 8] * 1.4426950408889634f : CUDART_INF_F;
-        for (; cons.tile < cons.end; cons.tile += kWarps) {
-            int key0;
-            const int nk = w.keys(cons.b, cons.r, (int)(cons.tile - cons.seg), cons.len, key0);
-            if (nk == 0) continue;
+        for (int i = 4 * cons.pos + warp; i < 4 * cons.end; i += kWThreads / 32) {
+            const int blk = w.key0(cons.b, cons.r, i / 4 - cons.seg, cons.len);
+            const int key0 = blk + kTile * (i & 3), nk = min(kTile, cons.len - key0);
+            if (blk < 0 || nk <= 0) continue;
             const int64_t row = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max + key0;
             float x[4][4];
             scores<DH>(a.k_codes + row * C::CODE, a.k_scales + row * C::NG, qf, g, t, x);
@@ -611,7 +717,7 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
         kv4_decay_kernel<<<dim3(8, a.B * a.H_kv), 256, 0, s>>>(a);
         note_launch(1);
     }
-    kv4_weights_kernel<DH><<<2 * kKv4Ctas, kThreads, 0, s>>>(a);
+    kv4_weights_kernel<DH><<<2 * kKv4Ctas, kWThreads, 0, s>>>(a);
     note_launch(1);
     trace_end(s, MSA_KERNEL_KV4_WEIGHTS);
     return cudaGetLastError();

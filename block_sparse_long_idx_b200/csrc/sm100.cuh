@@ -315,6 +315,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// Orders this thread's shared-memory accesses before later bulk copies to the same memory.
+__device__ __forceinline__ void fence_proxy_async()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // 32-byte global store of w[0..7] (the address must be 32-byte aligned).
 __device__ __forceinline__ void st_global_v8(uint32_t* p, const uint32_t* w)
 {
