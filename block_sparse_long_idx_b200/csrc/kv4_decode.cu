@@ -34,8 +34,15 @@ namespace {
 
 constexpr int kBlocks = 3;          // blocks of a chunk
 constexpr int kStages = 3;          // chunks of the ring
-constexpr int kWarps = 4 * kBlocks; // a warp takes 32 keys of a chunk
+constexpr int kWarps = 4 * kBlocks; // consumer warps: each takes 32 keys of a chunk
 constexpr int kThreads = kWarps * 32;
+constexpr int kLaunch = kThreads + 128; // and one warpgroup whose first thread starts the copies
+constexpr int kRegs = 160, kProducerRegs = 32; // of the 128 a thread is launched with
+static_assert(kThreads * kRegs + 128 * kProducerRegs <= kLaunch * 128, "register split");
+#ifndef KPAD
+#define KPAD 4
+#endif
+constexpr int kJoin = KPAD; // what joining a segment costs, in blocks: it counts in the split of the work
 constexpr int kSlots = kWarps / 2; // join scratch: one output per pair of warps
 constexpr int kTile = 32;          // keys of a warp's part
 constexpr float kHeadroom = 7.f;   // P's reference: log2 units below the maximum it was set from
@@ -54,30 +61,27 @@ struct Cfg {
     static constexpr int SMEM = kStages * STAGE + (WARPS > PARTS ? WARPS : PARTS) * 4;
 };
 
-struct Shared {
-    uint64_t full[kStages], empty[kStages];
-    float m[kSlots][16], l[kSlots][16];
-    float part_l[16];
-    int warp_blocks[kWarps];
-    int b0, seg0; // sequence holding the slice's first block, first block of that sequence
-    int last;     // this CTA joins the partials of the segment
-    int abort_flag;
-};
-
-// The flattened list: sequence b owns H_kv * blocks(b) blocks, KV head by KV head. With given blocks
-// every KV head has k, padding among them.
+// The flattened list: a segment is a (sequence, KV head); sequence b owns H_kv segments of kJoin units (no
+// work, they stand for the join) and blocks(b) blocks. With given blocks every segment has k, padding
+// among them.
+template <bool GIVEN>
 struct Work {
     const Kv4DecodeArgs& a;
     __device__ __forceinline__ bool valid(int len) const { return len >= a.min_len && len <= a.L_max; }
     __device__ __forceinline__ int blocks(int len) const // per KV head
     {
         if (!valid(len) || len == 0) return 0;
-        return a.block_idx ? a.k : (len + kBk - 1) / kBk;
+        return GIVEN ? a.k : (len + kBk - 1) / kBk;
+    }
+    __device__ __forceinline__ int units(int len) const // per segment
+    {
+        const int n = blocks(len);
+        return n > 0 ? n + kJoin : 0;
     }
     // First key of entry i of (b, r); -1 for padding and for entries the check reports.
     __device__ __forceinline__ int key0(int b, int r, int i, int len) const
     {
-        if (!a.block_idx) return i * kBk;
+        if (!GIVEN) return i * kBk;
         const int32_t* sel = a.block_idx + ((int64_t)b * a.H_kv + r) * a.k;
         const int blk = sel[i];
         if (blk < 0 || blk > (len - 1) / kBk || (i > 0 && blk <= sel[i - 1])) return -1;
@@ -85,74 +89,88 @@ struct Work {
     }
 };
 
-// Block-wide: the number of blocks of all sequences (below 2^31, checked on the host for full caches).
-// Sequences [b_lo, b_hi) are the calling thread's, `before` the blocks of those before them.
-template <int THREADS>
-__device__ __forceinline__ int total_blocks(const Work& w, int* warp_blocks, int& before, int& b_lo, int& b_hi)
+// Block-wide: the number of units of all sequences (below 2^31, checked on the host for full caches).
+// Sequences [b_lo, b_hi) are the calling thread's, `before` the units of those before them.
+template <int THREADS, bool GIVEN>
+__device__ __forceinline__ int total_units(const Work<GIVEN>& w, int* warp_units, int& before, int& b_lo, int& b_hi)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (w.a.B + THREADS - 1) / THREADS;
     b_lo = min(w.a.B, tid * per);
     b_hi = min(w.a.B, b_lo + per);
     int n = 0;
-    for (int b = b_lo; b < b_hi; ++b) n += w.blocks(w.a.lens[b]) * w.a.H_kv;
+    for (int b = b_lo; b < b_hi; ++b) n += w.units(w.a.lens[b]) * w.a.H_kv;
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) warp_blocks[warp] = x;
+    if (lane == 31) warp_units[warp] = x;
     __syncthreads();
     int total = 0;
     before = x - n;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
-        const int y = warp_blocks[i];
+        const int y = warp_units[i];
         if (i < warp) before += y;
         total += y;
     }
     return total;
 }
 
-// A walk over the slice [lo, hi), segment by segment (a segment is a (sequence, KV head)).
+// A walk over the slice [lo, hi) of the list, segment by segment.
+template <bool GIVEN>
 struct Walk {
     int b, r, len, n; // sequence, KV head, length, blocks of a segment of this sequence
-    int seg;          // first block of the segment
+    int seg;          // first block of the segment, behind its kJoin units
     int lo, hi;       // the slice
-    int pos, end;     // the part of the segment in the slice, from the next block on
+    int pos, end;     // the part of the segment in the slice, from the next block on (pos >= end: none)
 
     __device__ __forceinline__ void enter()
     {
         pos = max(seg, lo);
         end = min(seg + n, hi);
     }
-    __device__ __forceinline__ void begin(const Work& w, int b0, int seq0, int lo_, int hi_)
+    __device__ __forceinline__ void begin(const Work<GIVEN>& w, int b0, int seq0, int lo_, int hi_)
     {
         lo = lo_;
         hi = hi_;
         b = b0;
         len = w.a.lens[b];
         n = w.blocks(len);
-        r = (lo - seq0) / n;
-        seg = seq0 + r * n;
+        r = (lo - seq0) / (n + kJoin);
+        seg = seq0 + r * (n + kJoin) + kJoin;
         enter();
     }
     __device__ __forceinline__ bool more() const { return seg < hi; }
-    __device__ __forceinline__ void next_segment(const Work& w)
+    __device__ __forceinline__ void next_segment(const Work<GIVEN>& w)
     {
-        seg += n;
+        seg += n + kJoin;
         if (++r == w.a.H_kv) {
             r = 0;
-            if (seg < hi) {
+            if (seg < hi) { // the list goes on
+                int m;
                 do {
                     len = w.a.lens[++b];
-                    n = w.blocks(len);
-                } while (n == 0);
+                    m = w.blocks(len);
+                } while (m == 0);
+                n = m;
             }
         }
         enter();
     }
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    float m[kSlots][16], l[kSlots][16];
+    float part_l[16];
+    uint4 q[8][32]; // Q fragments of the segment
+    int warp_units[kLaunch / 32];
+    int b0, seg0; // sequence holding the slice's first unit, first unit of that sequence
+    int last;     // this CTA joins the partials of the segment
+    int abort_flag;
 };
 
 // A fragments of q's rows g and g + 8 (rows past the G heads are zero) in fp16, and the factors that
@@ -190,9 +208,8 @@ __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int
 // x[n][e] = the fp32 sums of q's rows (e < 2: g, else g + 8) with key 8 n + t + 4 (e & 1) of a tile
 // whose codes and scales start at kc and ks (column 2u of step n is key 8 n + u, column 2u + 1 key
 // 8 n + u + 4, which spreads O's reads of V over the shared-memory banks).
-template <int DH>
-__device__ __forceinline__ void scores(const uint8_t* kc, const uint8_t* ks, const uint32_t (&qf)[DH / 16][4], int g, int t,
-                                       float (&x)[4][4])
+template <int DH, class Q>
+__device__ __forceinline__ void scores(const uint8_t* kc, const uint8_t* ks, const Q& qget, int g, int t, float (&x)[4][4])
 {
     uint32_t c[4][DH / 32], s[4][DH / 64];
     const int row = (g >> 1) + 4 * (g & 1);
@@ -216,16 +233,25 @@ __device__ __forceinline__ void scores(const uint8_t* kc, const uint8_t* ks, con
     }
 #pragma unroll
     for (int i = 0; i < DH / 32; ++i) {
-        uint32_t h[4][4];
+        uint32_t h[4][4], qa[4], qb[4];
+        qget(2 * i, qa);
+        qget(2 * i + 1, qb);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             e2m1x8_to_f16x2(c[n][i], h[n]);
-            mma_f16_16816(x[n], qf[2 * i], mul_f16x2(h[n][0], s[n][i / 2]), mul_f16x2(h[n][1], s[n][i / 2]));
+            mma_f16_16816(x[n], qa, mul_f16x2(h[n][0], s[n][i / 2]), mul_f16x2(h[n][1], s[n][i / 2]));
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-            mma_f16_16816(x[n], qf[2 * i + 1], mul_f16x2(h[n][2], s[n][i / 2]), mul_f16x2(h[n][3], s[n][i / 2]));
+            mma_f16_16816(x[n], qb, mul_f16x2(h[n][2], s[n][i / 2]), mul_f16x2(h[n][3], s[n][i / 2]));
     }
+}
+
+__device__ __forceinline__ uint4 lds128(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)));
+    return v;
 }
 
 // ex2(-inf) = 0 keeps empty rows and tiles out of the joins.
@@ -238,8 +264,11 @@ __device__ __forceinline__ void store_out(const Kv4DecodeArgs& a, int64_t row, i
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-template <int DH>
-__global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a)
+// The consumers' barrier (the producer's warpgroup takes no part).
+__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+template <int DH, bool GIVEN>
+__global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
 {
     using C = Cfg<DH>;
     constexpr int KS = DH / 16; // contraction steps of S
@@ -249,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
     float* join = reinterpret_cast<float*>(ring + kStages * C::STAGE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.H_q / a.H_kv;
-    const Work w{a};
+    const Work<GIVEN> w{a};
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -260,12 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
         sh.abort_flag = 0;
     }
     int before, b_lo, b_hi;
-    const int total = total_blocks<kThreads>(w, sh.warp_blocks, before, b_lo, b_hi);
-    const int n_cta = min((total + kBlocks - 1) / kBlocks, (int)gridDim.x); // a chunk for every CTA where there are that many
+    const int total = total_units<kLaunch>(w, sh.warp_units, before, b_lo, b_hi);
+    const int n_cta = min((total + kJoin + kBlocks - 1) / (kJoin + kBlocks), (int)gridDim.x); // a chunk or more for each
     const int cta = blockIdx.x;
-    // sequences without keys have no blocks: the last CTA answers for them, and reports what is rejected
+    // sequences without keys have no units: the last CTA answers for them, and reports what is rejected
     if (cta == (int)gridDim.x - 1) {
-        for (int b = warp; b < a.B; b += kWarps) {
+        for (int b = warp; b < a.B; b += kLaunch / 32) {
             const int len = a.lens[b];
             if (!w.valid(len)) {
                 if (lane == 0) report_error(a.err, MSA_ERR_DEVICE_CHECK, 200 + b);
@@ -274,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                     reinterpret_cast<uint32_t*>(a.out + (int64_t)b * a.H_q * DH)[e] = 0u;
                 if (a.lse)
                     for (int e = lane; e < a.H_q; e += 32) a.lse[(int64_t)b * a.H_q + e] = -CUDART_INF_F;
-            } else if (a.block_idx) {
+            } else if (GIVEN) {
                 for (int e = lane; e < a.H_kv * a.k; e += 32) {
                     const int r = e / a.k, i = e % a.k;
                     if (w.key0(b, r, i, len) < 0 && a.block_idx[(int64_t)b * a.H_kv * a.k + e] != -1)
@@ -286,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
     if (cta >= n_cta) return;
     const int lo = (int)((int64_t)total * cta / n_cta), hi = (int)((int64_t)total * (cta + 1) / n_cta);
     for (int b = b_lo; b < b_hi; ++b) {
-        const int n = w.blocks(a.lens[b]) * a.H_kv;
+        const int n = w.units(a.lens[b]) * a.H_kv;
         if (lo >= before && lo < before + n) {
             sh.b0 = b;
             sh.seg0 = before;
@@ -296,67 +325,88 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
     __syncthreads();
 
     volatile int* abort_flag = &sh.abort_flag;
-    Walk prod, cons;
+    Walk<GIVEN> cons;
     cons.begin(w, sh.b0, sh.seg0, lo, hi);
-    prod = cons;
-    uint32_t issued = 0, used = 0; // chunks
-    // Lane 0 of warp 0 starts the copies of the next chunk: up to kBlocks blocks of one segment, the
-    // visible rows rounded up to 32 (L_max is whole blocks).
-    auto issue = [&] {
-        if (!prod.more()) return true;
-        const uint32_t st = issued % kStages, round = issued / kStages;
-        if (round > 0 && !wait_or_abort(&sh.empty[st], (round - 1) & 1, abort_flag, a.err, 62, kWaitLimit)) return false;
-        uint8_t* s = ring + st * C::STAGE;
-        const int64_t row0 = ((int64_t)prod.b * a.H_kv + prod.r) * a.L_max;
-        const int nb = min(kBlocks, prod.end - prod.pos);
-        auto copy = [&](int key, int at, int rows) {
-            bulk_load(s + C::K_CODES + at * C::CODE, a.k_codes + (row0 + key) * C::CODE, rows * C::CODE, &sh.full[st]);
-            bulk_load(s + C::K_SCALES + at * C::NG, a.k_scales + (row0 + key) * C::NG, rows * C::NG, &sh.full[st]);
-            bulk_load(s + C::V_CODES + at * C::CODE, a.v_codes + (row0 + key) * C::CODE, rows * C::CODE, &sh.full[st]);
-            bulk_load(s + C::V_SCALES + at * C::NG, a.v_scales + (row0 + key) * C::NG, rows * C::NG, &sh.full[st]);
-        };
-        if (!a.block_idx) {
-            const int key = (prod.pos - prod.seg) * kBk;
-            const int rows = min(nb * kBk, (prod.len - key + kTile - 1) / kTile * kTile);
-            mbar_arrive_expect_tx(&sh.full[st], rows * 2 * (C::CODE + C::NG));
-            copy(key, 0, rows);
-        } else {
-            int key[kBlocks], rows[kBlocks], all = 0;
-#pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                key[i] = i < nb ? w.key0(prod.b, prod.r, prod.pos - prod.seg + i, prod.len) : -1;
-                rows[i] = key[i] < 0 ? 0 : min(kBk, (prod.len - key[i] + kTile - 1) / kTile * kTile);
-                all += rows[i];
-            }
-            mbar_arrive_expect_tx(&sh.full[st], all * 2 * (C::CODE + C::NG));
-#pragma unroll
-            for (int i = 0; i < kBlocks; ++i)
-                if (rows[i] > 0) copy(key[i], i * kBk, rows[i]);
-        }
-        ++issued;
-        prod.pos += nb;
-        if (prod.pos >= prod.end) prod.next_segment(w);
-        return true;
-    };
-    bool ok = true;
-    if (tid == 0)
-        for (int i = 0; i < kStages - 1; ++i) ok = issue() && ok;
 
+    if (warp >= kWarps) {
+        // ---------------------------------------------------------------- producer
+        reg_dealloc<kProducerRegs>();
+        if (tid != kThreads) return;
+        uint32_t n = 0; // chunks
+        bool ok = true;
+        for (; ok && cons.more(); cons.next_segment(w)) {
+            const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
+            for (; cons.pos < cons.end; cons.pos += kBlocks, ++n) {
+                const uint32_t st = n % kStages, round = n / kStages;
+                if (round > 0 && !wait_or_abort(&sh.empty[st], (round - 1) & 1, abort_flag, a.err, 62, kWaitLimit)) {
+                    ok = false;
+                    break;
+                }
+                // up to kBlocks blocks of the segment, the visible rows rounded up to 32 (L_max is whole blocks)
+                uint8_t* s = ring + st * C::STAGE;
+                const int nb = min(kBlocks, cons.end - cons.pos);
+                auto copy = [&](int key, int at, int rows) {
+                    bulk_load(s + C::K_CODES + at * C::CODE, a.k_codes + (row0 + key) * C::CODE, rows * C::CODE, &sh.full[st]);
+                    bulk_load(s + C::K_SCALES + at * C::NG, a.k_scales + (row0 + key) * C::NG, rows * C::NG, &sh.full[st]);
+                    bulk_load(s + C::V_CODES + at * C::CODE, a.v_codes + (row0 + key) * C::CODE, rows * C::CODE, &sh.full[st]);
+                    bulk_load(s + C::V_SCALES + at * C::NG, a.v_scales + (row0 + key) * C::NG, rows * C::NG, &sh.full[st]);
+                };
+                auto rows_of = [&](int key, int most) { return min(most, (cons.len - key + kTile - 1) / kTile * kTile); };
+                if (!GIVEN) {
+                    const int key = (cons.pos - cons.seg) * kBk, rows = rows_of(key, nb * kBk);
+                    mbar_arrive_expect_tx(&sh.full[st], rows * 2 * (C::CODE + C::NG));
+                    copy(key, 0, rows);
+                } else {
+                    int key[kBlocks], all = 0;
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i) {
+                        key[i] = i < nb ? w.key0(cons.b, cons.r, cons.pos - cons.seg + i, cons.len) : -1;
+                        if (key[i] >= 0) all += rows_of(key[i], kBk);
+                    }
+                    mbar_arrive_expect_tx(&sh.full[st], all * 2 * (C::CODE + C::NG));
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+                        if (key[i] >= 0) copy(key[i], i * kBk, rows_of(key[i], kBk));
+                }
+            }
+        }
+        // after an abort, copies may still be in flight: the shared memory must outlive them
+        if (!ok)
+            for (uint32_t m = n > kStages ? n - kStages : 0; m < n; ++m)
+                drain_wait(&sh.full[m % kStages], (m / kStages) & 1, a.err, 61, kWaitLimit);
+        return;
+    }
+    // -------------------------------------------------------------------- consumers
+    reg_alloc<kRegs>();
+    auto leave = [&](uint32_t st) {
+        __syncwarp(); // every lane has read the stage
+        if (lane == 0) mbar_arrive(&sh.empty[st]);
+    };
+    uint32_t used = 0; // chunks
+    bool ok = true;
     for (; cons.more(); cons.next_segment(w)) {
+        if (cons.pos >= cons.end) continue;
         uint32_t qf[KS][4];
         float f0, f1;
         load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
+        if (warp == 0)
+            for (int i = 0; i < KS; ++i) sh.q[i][lane] = make_uint4(qf[i][0], qf[i][1], qf[i][2], qf[i][3]);
+        sync_consumers();
+        auto qget = [&](int i, uint32_t (&v)[4]) {
+            const uint4 u = lds128(&sh.q[i][lane]);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+        };
         float o[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f; // references, this lane's sums
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F; // references
+        uint64_t l0 = 0, l1 = 0;                      // this lane's sums, as pairs of even and odd columns
 
         for (; ok && cons.pos < cons.end; cons.pos += kBlocks, ++used) {
-            if (tid == 0) ok = issue();
             const uint32_t st = used % kStages;
-            ok = ok && wait_or_abort(&sh.full[st], (used / kStages) & 1, abort_flag, a.err, 60, kWaitLimit);
+            ok = wait_or_abort(&sh.full[st], (used / kStages) & 1, abort_flag, a.err, 60, kWaitLimit);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             int nk = 0; // visible keys of the warp's 32
@@ -365,13 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                 if (key >= 0) nk = min(kTile, cons.len - key - kTile * (warp & 3));
             }
             if (nk <= 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.empty[st]);
+                leave(st);
                 continue;
             }
             const uint8_t* s = ring + st * C::STAGE;
             float x[4][4];
-            scores<DH>(s + C::K_CODES + warp * kTile * C::CODE, s + C::K_SCALES + warp * kTile * C::NG, qf, g, t, x);
+            scores<DH>(s + C::K_CODES + warp * kTile * C::CODE, s + C::K_SCALES + warp * kTile * C::NG, qget, g, t, x);
             const uint8_t* vc = s + C::V_CODES + warp * kTile * C::CODE;
             uint8_t* vs = ring + st * C::STAGE + C::V_SCALES + warp * kTile * C::NG;
             // ------------------------------------------------------------ softmax
@@ -394,21 +443,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             mx1 = max3f(mx1, x[2][3], x[3][2]);
             mx0 = fmaxf(mx0, x[3][1]);
             mx1 = fmaxf(mx1, x[3][3]);
+            // the references (equal in the 4 lanes of a row) move up only when P would leave [0, 2^15): exact, and rare
+            if (__any_sync(0xffffffffu, mx0 * f0 > m0 + kRaise || mx1 * f1 > m1 + kRaise)) { // f > 0
 #pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-            }
-            mx0 *= f0; // f > 0
-            mx1 *= f1;
-            // the references move up only when P would leave [0, 2^15): exact, and rare
-            if (__any_sync(0xffffffffu, mx0 > m0 + kRaise || mx1 > m1 + kRaise)) {
+                for (int d = 1; d < 4; d <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+                }
+                mx0 *= f0;
+                mx1 *= f1;
                 const float n0 = mx0 > m0 + kRaise ? mx0 - kHeadroom : m0, n1 = mx1 > m1 + kRaise ? mx1 - kHeadroom : m1;
                 const float r0 = join_weight(m0, n0), r1 = join_weight(m1, n1);
                 m0 = n0;
                 m1 = n1;
-                l0 *= r0;
-                l1 *= r1;
+                l0 = f2_mul(l0, f2_pack(r0, r0));
+                l1 = f2_mul(l1, f2_pack(r1, r1));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     o[n][0] *= r0;
@@ -418,12 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                 }
             }
             uint32_t pf[2][4];
+            const uint64_t ff0 = f2_pack(f0, f0), ff1 = f2_pack(f1, f1), mm0 = f2_pack(-m0, -m0), mm1 = f2_pack(-m1, -m1);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const float p0 = ex2_approx(fmaf(x[n][0], f0, -m0)), p1 = ex2_approx(fmaf(x[n][1], f0, -m0));
-                const float p2 = ex2_approx(fmaf(x[n][2], f1, -m1)), p3 = ex2_approx(fmaf(x[n][3], f1, -m1));
-                l0 += p0 + p1;
-                l1 += p2 + p3;
+                const uint64_t y0 = f2_fma(f2_pack(x[n][0], x[n][1]), ff0, mm0), y1 = f2_fma(f2_pack(x[n][2], x[n][3]), ff1, mm1);
+                const float p0 = ex2_approx(f2_lo(y0)), p1 = ex2_approx(f2_hi(y0));
+                const float p2 = ex2_approx(f2_lo(y1)), p3 = ex2_approx(f2_hi(y1));
+                l0 = f2_add(l0, f2_pack(p0, p1));
+                l1 = f2_add(l1, f2_pack(p2, p3));
                 pf[n >> 1][(n & 1) * 2] = pack_f16x2(p0, p1);
                 pf[n >> 1][(n & 1) * 2 + 1] = pack_f16x2(p2, p3);
             }
@@ -462,14 +513,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                                       mul_f16x2(b1[e & 1][e >> 1], sc[1]));
                 }
             }
-            __syncwarp(); // every lane has read the stage
-            if (lane == 0) mbar_arrive(&sh.empty[st]);
+            leave(st);
         }
         // ------------------------------------------------------------ join the warps
+        float s0 = f2_lo(l0) + f2_hi(l0), s1 = f2_lo(l1) + f2_hi(l1);
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+            s0 += __shfl_xor_sync(0xffffffffu, s0, d);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, d);
         }
         // two steps: the upper half of the warps hand theirs to the lower half
         float* mine = join + (warp % kSlots) * C::WARP + t * C::LANE;
@@ -477,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             if (t == 0) {
                 sh.m[warp % kSlots][g] = m0;
                 sh.m[warp % kSlots][g + 8] = m1;
-                sh.l[warp % kSlots][g] = l0;
-                sh.l[warp % kSlots][g + 8] = l1;
+                sh.l[warp % kSlots][g] = s0;
+                sh.l[warp % kSlots][g + 8] = s1;
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) // row g + 8 half: elements t * DH / 4 + (0 .. DH / 4)
@@ -490,11 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                             o[n][2 * half + c], o[n + 1][2 * half + c], o[n + 2][2 * half + c], o[n + 3][2 * half + c]);
         };
         if (warp >= kSlots) put();
-        __syncthreads();
+        sync_consumers();
         if (warp < kSlots) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float &m = half ? m1 : m0, &l = half ? l1 : l0;
+                float &m = half ? m1 : m0, &l = half ? s1 : s0;
                 const float om = sh.m[warp][g + 8 * half], M = fmaxf(m, om);
                 const float wa = join_weight(m, M), wb = join_weight(om, M);
                 l = fmaf(wa, l, wb * sh.l[warp][g + 8 * half]);
@@ -513,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             __syncwarp(); // every lane has read the rows' maxima and sums
             put();
         }
-        __syncthreads();
+        sync_consumers();
         const bool whole = cons.seg >= lo && cons.seg + cons.n <= hi; // no other CTA has tiles of it
         float* part = a.parts + (int64_t)(2 * cta + (cons.seg > lo ? 1 : 0)) * kKv4PartFloats;
         for (int e = tid; e < G * (DH / 4); e += kThreads) {
@@ -546,13 +597,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
             }
         }
         if (!whole) {
-            // the CTAs with tiles of this segment: that of its first tile .. that of its last
+            // the CTAs with blocks of this segment: that of its first block .. that of its last
             const int c0 = (int)(((int64_t)(cons.seg + 1) * n_cta - 1) / total);
             const int c1 = (int)(((int64_t)(cons.seg + cons.n) * n_cta - 1) / total);
             __threadfence();
-            __syncthreads();
+            sync_consumers();
             if (tid == 0) sh.last = atomicAdd(&a.arrived[c0], 1) == c1 - c0;
-            __syncthreads();
+            sync_consumers();
             if (sh.last) {
                 __threadfence();
                 const int np = c1 - c0 + 1;
@@ -567,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                     cw[c * 16 + row] = row < G ? __ldcg(slot(c) + 16 * 128 + row) : -CUDART_INF_F;
                     cl[c * 16 + row] = row < G ? __ldcg(slot(c) + 16 * 128 + 16 + row) : 0.f;
                 }
-                __syncthreads();
+                sync_consumers();
                 for (int row = warp; row < G; row += kWarps) {
                     float M = -CUDART_INF_F, L = 0.f;
                     for (int c = lane; c < np; c += 32) M = fmaxf(M, cw[c * 16 + row]);
@@ -587,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                                 L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -CUDART_INF_F;
                     }
                 }
-                __syncthreads();
+                sync_consumers();
                 // groups of threads take every (number of groups)-th partial, each thread up to 4 x 4 elements
                 const int n4 = G * (DH / 4), width = n4 >= 128 ? 128 : (n4 >= 64 ? 64 : 32), groups = kThreads / width;
                 const int grp = tid / width, e0 = tid % width;
@@ -612,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     if (e0 + u * width < n4) s4[grp * n4 + e0 + u * width] = acc[u];
-                __syncthreads();
+                sync_consumers();
                 for (int e = tid; e < n4; e += kThreads) {
                     float4 v = s4[e];
                     for (int i = 1; i < groups; ++i) {
@@ -624,31 +675,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(Kv4DecodeArgs a
                 }
             }
         }
-        __syncthreads(); // the join scratch is free again
+        sync_consumers(); // the join scratch is free again
     }
-    // after an abort, copies may still be in flight: the shared memory must outlive them
-    if (tid == 0)
-        for (; used < issued; ++used) drain_wait(&sh.full[used % kStages], (used / kStages) & 1, a.err, 61, kWaitLimit);
 }
 
 // Accumulated weights, after the attention (they need the final lse): K is read once more, and every
 // visible key of the list gets its group's sum of softmax weights. A warp takes 32 keys at a time.
 constexpr int kWThreads = 256;
 
-template <int DH>
+template <int DH, bool GIVEN>
 __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs a)
 {
     using C = Cfg<DH>;
-    __shared__ int warp_blocks[kWThreads / 32], b0, seg0;
+    __shared__ int warp_units[kWThreads / 32], b0, seg0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.H_q / a.H_kv;
-    const Work w{a};
+    const Work<GIVEN> w{a};
     int before, b_lo, b_hi;
-    const int total = total_blocks<kWThreads>(w, warp_blocks, before, b_lo, b_hi);
+    const int total = total_units<kWThreads>(w, warp_units, before, b_lo, b_hi);
     const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
     if (lo >= hi) return;
     for (int b = b_lo; b < b_hi; ++b) {
-        const int n = w.blocks(a.lens[b]) * a.H_kv;
+        const int n = w.units(a.lens[b]) * a.H_kv;
         if (lo >= before && lo < before + n) {
             b0 = b;
             seg0 = before;
@@ -656,8 +704,9 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         before += n;
     }
     __syncthreads();
-    Walk cons;
+    Walk<GIVEN> cons;
     for (cons.begin(w, b0, seg0, lo, hi); cons.more(); cons.next_segment(w)) {
+        if (cons.pos >= cons.end) continue;
         uint32_t qf[DH / 16][4];
         float f0, f1;
         load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
@@ -670,7 +719,8 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
             if (blk < 0 || nk <= 0) continue;
             const int64_t row = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max + key0;
             float x[4][4];
-            scores<DH>(a.k_codes + row * C::CODE, a.k_scales + row * C::NG, qf, g, t, x);
+            auto qget = [&](int i, uint32_t (&v)[4]) { v[0] = qf[i][0], v[1] = qf[i][1], v[2] = qf[i][2], v[3] = qf[i][3]; };
+            scores<DH>(a.k_codes + row * C::CODE, a.k_scales + row * C::NG, qget, g, t, x);
             float mine = 0.f; // lane (g, t): key 8 (g / 2) + t + 4 (g % 2)
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -684,7 +734,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
             const int key = 8 * (g >> 1) + t + 4 * (g & 1);
             if (key < nk) {
                 // given blocks: kv4_decay_kernel has written decay * w_in to every visible key
-                const float old = a.block_idx ? a.w_out[row + key] : (a.w_in ? a.decay * a.w_in[row + key] : 0.f);
+                const float old = GIVEN ? a.w_out[row + key] : (a.w_in ? a.decay * a.w_in[row + key] : 0.f);
                 a.w_out[row + key] = old + mine;
             }
         }
@@ -702,22 +752,22 @@ __global__ void __launch_bounds__(256) kv4_decay_kernel(Kv4DecodeArgs a)
         a.w_out[base + j] = a.w_in ? a.decay * a.w_in[base + j] : 0.f;
 }
 
-template <int DH>
+template <int DH, bool GIVEN>
 cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DH>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<DH, GIVEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DH>::SMEM);
     if (e != cudaSuccess) return e;
     trace_begin(s);
-    kv4_decode_kernel<DH><<<kKv4Ctas, kThreads, Cfg<DH>::SMEM, s>>>(a);
+    kv4_decode_kernel<DH, GIVEN><<<kKv4Ctas, kLaunch, Cfg<DH>::SMEM, s>>>(a);
     trace_end(s, MSA_KERNEL_KV4_ATTN);
     note_launch(1);
     if (!a.w_out) return cudaGetLastError();
     trace_begin(s);
-    if (a.block_idx && !(a.w_in == a.w_out && a.decay == 1.f)) {
+    if (GIVEN && !(a.w_in == a.w_out && a.decay == 1.f)) {
         kv4_decay_kernel<<<dim3(8, a.B * a.H_kv), 256, 0, s>>>(a);
         note_launch(1);
     }
-    kv4_weights_kernel<DH><<<2 * kKv4Ctas, kWThreads, 0, s>>>(a);
+    kv4_weights_kernel<DH, GIVEN><<<2 * kKv4Ctas, kWThreads, 0, s>>>(a);
     note_launch(1);
     trace_end(s, MSA_KERNEL_KV4_WEIGHTS);
     return cudaGetLastError();
@@ -727,7 +777,8 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s)
 {
-    return a.d_h == 128 ? launch<128>(a, s) : launch<64>(a, s);
+    if (a.block_idx) return a.d_h == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
+    return a.d_h == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
 }
 
 } // namespace msa

@@ -1029,7 +1029,7 @@ static msa_status kv4_check(const msa_kv4_cache* c)
         return MSA_ERR_INVALID_ARG;
     if (!(c->d_h == 64 || c->d_h == 128) || c->L_max % kBk != 0 || c->L_max > kMaxN || c->B > 65535 || c->H_kv > 65535)
         return MSA_ERR_UNSUPPORTED;
-    // tiles of all sequences are counted in 32 bits, KV heads of all sequences are a grid dimension
+    // units of work (blocks, and some for every KV head) are counted in 32 bits, KV heads are a grid dimension
     if ((int64_t)c->B * c->H_kv > 65535 || (int64_t)c->B * c->H_kv * (c->L_max / 32) > 0x7FFFFFFF) return MSA_ERR_UNSUPPORTED;
     return MSA_OK;
 }

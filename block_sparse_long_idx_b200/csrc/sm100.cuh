@@ -315,6 +315,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// Adds to a shared-memory word; orders the CTA's accesses before it and after it. Returns the old value.
+__device__ __forceinline__ int atom_add_acq_rel_cta(int* p, int v)
+{
+    int old;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(p)), "r"(v) : "memory");
+    return old;
+}
+
 // Orders this thread's shared-memory accesses before later bulk copies to the same memory.
 __device__ __forceinline__ void fence_proxy_async()
 {
