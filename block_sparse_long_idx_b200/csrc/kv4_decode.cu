@@ -56,9 +56,9 @@ struct Cfg {
                          STAGE = V_SCALES + KEYS * NG;
     // join scratch: [slot][16 rows][4 lanes][DH / 4], padded so that 16-byte accesses do not conflict
     static constexpr int LANE = DH / 4 + 4, ROW = 4 * LANE, WARP = 16 * ROW;
-    // the join of several CTAs' partials uses the same memory: weights and sums [kKv4Ctas][16], thread groups' outputs
-    static constexpr int WARPS = kSlots * WARP, PARTS = kKv4Ctas * 32 + kThreads / 128 * 16 * DH;
-    static constexpr int SMEM = kStages * STAGE + (WARPS > PARTS ? WARPS : PARTS) * 4;
+    static constexpr int SMEM = kStages * STAGE + kSlots * WARP * 4;
+    // the join of several CTAs' partials uses it for its groups of threads (at most 12): outputs, maxima and sums
+    static_assert(kThreads / 128 * 16 * DH + kThreads / 32 * 32 <= kSlots * WARP, "scratch of the partials' join");
 };
 
 // The flattened list: a segment is a (sequence, KV head); sequence b owns H_kv segments of kJoin units (no
@@ -165,7 +165,6 @@ struct Walk {
 struct Shared {
     uint64_t full[kStages], empty[kStages];
     float m[kSlots][16], l[kSlots][16];
-    float part_l[16];
     uint4 q[8][32]; // Q fragments of the segment
     int warp_units[kLaunch / 32];
     int b0, seg0; // sequence holding the slice's first unit, first unit of that sequence
@@ -257,11 +256,25 @@ __device__ __forceinline__ uint4 lds128(const uint4* p)
 // ex2(-inf) = 0 keeps empty rows and tiles out of the joins.
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -CUDART_INF_F ? 0.f : ex2_approx(m - M); }
 
-// One output element run: 4 consecutive elements of one head.
-__device__ __forceinline__ void store_out(const Kv4DecodeArgs& a, int64_t row, int d, const float4& o, float inv)
+// Joins a partial (maximum m, sum l, outputs v) to (M, L, acc).
+__device__ __forceinline__ void merge(float& M, float& L, float4& acc, float m, float l, const float4& v)
 {
+    const float N = fmaxf(M, m), wa = join_weight(M, N), wb = join_weight(m, N);
+    M = N;
+    L = fmaf(wa, L, wb * l);
+    acc.x = fmaf(wa, acc.x, wb * v.x);
+    acc.y = fmaf(wa, acc.y, wb * v.y);
+    acc.z = fmaf(wa, acc.z, wb * v.z);
+    acc.w = fmaf(wa, acc.w, wb * v.w);
+}
+
+// Elements d .. d + 3 of one head, and its lse with element 0.
+__device__ __forceinline__ void finish(const Kv4DecodeArgs& a, int64_t row, int d, const float4& o, float M, float L)
+{
+    const float inv = L > 0.f ? a.v_scale / L : 0.f;
     *reinterpret_cast<uint2*>(a.out + row * a.d_h + d) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && d == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -CUDART_INF_F;
 }
 
 // The consumers' barrier (the producer's warpgroup takes no part).
@@ -585,9 +598,7 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 acc.w = fmaf(c, v.w, acc.w);
             }
             if (whole) {
-                const int64_t orow = (int64_t)cons.b * a.H_q + cons.r * G + row;
-                store_out(a, orow, q4 * 4, acc, L > 0.f ? a.v_scale / L : 0.f);
-                if (a.lse && q4 == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -CUDART_INF_F;
+                finish(a, (int64_t)cons.b * a.H_q + cons.r * G + row, q4 * 4, acc, M, L);
             } else {
                 *reinterpret_cast<float4*>(part + row * DH + q4 * 4) = acc;
                 if (q4 == 0) {
@@ -612,66 +623,42 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 const float* parts = a.parts + (int64_t)2 * c0 * kKv4PartFloats;
                 const int first = cons.seg > lo0 ? 1 : 0;
                 auto slot = [&](int c) { return parts + (int64_t)(c == 0 ? first : 2 * c) * kKv4PartFloats; };
-                float *cw = join, *cl = join + kKv4Ctas * 16, *sums = join + kKv4Ctas * 32;
-                for (int e = tid; e < np * 16; e += kThreads) {
-                    const int row = e % 16, c = e / 16;
-                    cw[c * 16 + row] = row < G ? __ldcg(slot(c) + 16 * 128 + row) : -CUDART_INF_F;
-                    cl[c * 16 + row] = row < G ? __ldcg(slot(c) + 16 * 128 + 16 + row) : 0.f;
-                }
-                sync_consumers();
-                for (int row = warp; row < G; row += kWarps) {
-                    float M = -CUDART_INF_F, L = 0.f;
-                    for (int c = lane; c < np; c += 32) M = fmaxf(M, cw[c * 16 + row]);
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                    for (int c = lane; c < np; c += 32) {
-                        const float wt = join_weight(cw[c * 16 + row], M);
-                        cw[c * 16 + row] = wt;
-                        L = fmaf(wt, cl[c * 16 + row], L);
-                    }
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-                    if (lane == 0) {
-                        sh.part_l[row] = L > 0.f ? a.v_scale / L : 0.f;
-                        if (a.lse)
-                            a.lse[(int64_t)cons.b * a.H_q + cons.r * G + row] =
-                                L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -CUDART_INF_F;
-                    }
-                }
-                sync_consumers();
-                // groups of threads take every (number of groups)-th partial, each thread up to 4 x 4 elements
+                // groups of threads take every (number of groups)-th partial, each thread up to 4 x 4 elements, with a
+                // running maximum, so that all loads of a step are independent
                 const int n4 = G * (DH / 4), width = n4 >= 128 ? 128 : (n4 >= 64 ? 64 : 32), groups = kThreads / width;
                 const int grp = tid / width, e0 = tid % width;
+                float M[4], L[4];
                 float4 acc[4] = {};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) M[u] = -CUDART_INF_F, L[u] = 0.f;
 #pragma unroll 4
                 for (int c = grp; c < np; c += groups) {
                     const float* p = slot(c);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const int e = e0 + u * width;
-                        if (e < n4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
-                            const float wt = cw[c * 16 + e / (DH / 4)];
-                            acc[u].x = fmaf(wt, v.x, acc[u].x);
-                            acc[u].y = fmaf(wt, v.y, acc[u].y);
-                            acc[u].z = fmaf(wt, v.z, acc[u].z);
-                            acc[u].w = fmaf(wt, v.w, acc[u].w);
-                        }
+                        const int e = min(e0 + u * width, n4 - 1), row = e / (DH / 4);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
+                        const float m = __ldcg(p + 16 * 128 + row), l = __ldcg(p + 16 * 128 + 16 + row);
+                        merge(M[u], L[u], acc[u], m, l, v);
                     }
                 }
-                float4* s4 = reinterpret_cast<float4*>(sums);
+                float4* s4 = reinterpret_cast<float4*>(join);
+                float2* ml = reinterpret_cast<float2*>(s4 + groups * n4);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (e0 + u * width < n4) s4[grp * n4 + e0 + u * width] = acc[u];
+                for (int u = 0; u < 4; ++u) {
+                    const int e = e0 + u * width;
+                    if (e < n4) {
+                        s4[grp * n4 + e] = acc[u];
+                        if (e % (DH / 4) == 0) ml[grp * 16 + e / (DH / 4)] = make_float2(M[u], L[u]);
+                    }
+                }
                 sync_consumers();
                 for (int e = tid; e < n4; e += kThreads) {
-                    float4 v = s4[e];
-                    for (int i = 1; i < groups; ++i) {
-                        const float4 y = s4[i * n4 + e];
-                        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-                    }
                     const int row = e / (DH / 4);
-                    store_out(a, (int64_t)cons.b * a.H_q + cons.r * G + row, e % (DH / 4) * 4, v, sh.part_l[row]);
+                    float Mr = -CUDART_INF_F, Lr = 0.f;
+                    float4 v = {};
+                    for (int i = 0; i < groups; ++i) merge(Mr, Lr, v, ml[i * 16 + row].x, ml[i * 16 + row].y, s4[i * n4 + e]);
+                    finish(a, (int64_t)cons.b * a.H_q + cons.r * G + row, e % (DH / 4) * 4, v, Mr, Lr);
                 }
             }
         }
