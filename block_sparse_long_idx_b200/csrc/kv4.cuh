@@ -78,6 +78,7 @@ struct Kv4RowsArgs {
     uint8_t* codes[2]; // K, V
     uint8_t* scales[2];
     float t[2];
+    float rt[2];       // 1 / t, or 0 (see quantise16)
     const uint16_t* x[2]; // append: [T][H_kv][d_h] bf16, rows x_stride[i] elements apart
     int64_t x_stride[2];
     uint16_t* y[2]; // read: [T][H_kv][d_h] bf16

@@ -204,29 +204,42 @@ __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int
     }
 }
 
-// x[n][e] = the fp32 sums of q's rows (e < 2: g, else g + 8) with key 8 n + t + 4 (e & 1) of a tile
-// whose codes and scales start at kc and ks (column 2u of step n is key 8 n + u, column 2u + 1 key
-// 8 n + u + 4, which spreads O's reads of V over the shared-memory banks).
+// A lane's part of 32 rows of K whose codes and scales start at kc and ks: of row 8 n + g / 2 + 4 (g % 2)
+// (column 2u of step n is key u, column 2u + 1 key u + 4) the codes of its run, and their scales.
+template <int DH>
+struct KTile {
+    uint32_t c[4][DH / 32];
+    uint16_t s[4];
+
+    __device__ __forceinline__ void load(const uint8_t* kc, const uint8_t* ks, int g, int t)
+    {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int key = 8 * n + (g >> 1) + 4 * (g & 1);
+            if constexpr (DH == 128) {
+                const uint4 v = *reinterpret_cast<const uint4*>(kc + key * 64 + t * 16);
+                c[n][0] = v.x, c[n][1] = v.y, c[n][2] = v.z, c[n][3] = v.w;
+                s[n] = *reinterpret_cast<const uint16_t*>(ks + key * 8 + t * 2);
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(kc + key * 32 + t * 8);
+                c[n][0] = v.x, c[n][1] = v.y;
+                s[n] = ks[key * 4 + t];
+            }
+        }
+    }
+};
+
+// x[n][e] = the fp32 sums of q's rows (e < 2: g, else g + 8) with key 8 n + t + 4 (e & 1) of the tile.
+// qget(i, a): the A fragment of step i.
 template <int DH, class Q>
-__device__ __forceinline__ void scores(const uint8_t* kc, const uint8_t* ks, const Q& qget, int g, int t, float (&x)[4][4])
+__device__ __forceinline__ void scores(const KTile<DH>& k, const Q& qget, float (&x)[4][4])
 {
-    uint32_t c[4][DH / 32], s[4][DH / 64];
-    const int row = (g >> 1) + 4 * (g & 1);
+    uint32_t s[4][DH / 64];
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        const int key = 8 * n + row;
-        if constexpr (DH == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kc + key * 64 + t * 16);
-            c[n][0] = v.x, c[n][1] = v.y, c[n][2] = v.z, c[n][3] = v.w;
-            const uint32_t sc = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + key * 8 + t * 2));
-            s[n][0] = prmt(sc, sc, 0x1010);
-            s[n][1] = prmt(sc, sc, 0x3232);
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kc + key * 32 + t * 8);
-            c[n][0] = v.x, c[n][1] = v.y;
-            const uint32_t sc = e4m3x2_to_f16x2(ks[key * 4 + t]);
-            s[n][0] = prmt(sc, sc, 0x1010);
-        }
+        const uint32_t sc = e4m3x2_to_f16x2(k.s[n]);
+        s[n][0] = prmt(sc, sc, 0x1010);
+        if constexpr (DH == 128) s[n][1] = prmt(sc, sc, 0x3232);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
     }
@@ -237,7 +250,7 @@ __device__ __forceinline__ void scores(const uint8_t* kc, const uint8_t* ks, con
         qget(2 * i + 1, qb);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            e2m1x8_to_f16x2(c[n][i], h[n]);
+            e2m1x8_to_f16x2(k.c[n][i], h[n]);
             mma_f16_16816(x[n], qa, mul_f16x2(h[n][0], s[n][i / 2]), mul_f16x2(h[n][1], s[n][i / 2]));
         }
 #pragma unroll
@@ -433,7 +446,11 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
             }
             const uint8_t* s = ring + st * C::STAGE;
             float x[4][4];
-            scores<DH>(s + C::K_CODES + warp * kTile * C::CODE, s + C::K_SCALES + warp * kTile * C::NG, qget, g, t, x);
+            {
+                KTile<DH> k;
+                k.load(s + C::K_CODES + warp * kTile * C::CODE, s + C::K_SCALES + warp * kTile * C::NG, g, t);
+                scores<DH>(k, qget, x);
+            }
             const uint8_t* vc = s + C::V_CODES + warp * kTile * C::CODE;
             uint8_t* vs = ring + st * C::STAGE + C::V_SCALES + warp * kTile * C::NG;
             // ------------------------------------------------------------ softmax
@@ -700,30 +717,50 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
         const float z0 = g < G ? lse[g] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
         const float z1 = g + 8 < G ? lse[g + 8] * 1.4426950408889634f : CUDART_INF_F;
-        for (int i = 4 * cons.pos + warp; i < 4 * cons.end; i += kWThreads / 32) {
-            const int blk = w.key0(cons.b, cons.r, i / 4 - cons.seg, cons.len);
-            const int key0 = blk + kTile * (i & 3), nk = min(kTile, cons.len - key0);
-            if (blk < 0 || nk <= 0) continue;
-            const int64_t row = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max + key0;
-            float x[4][4];
-            auto qget = [&](int i, uint32_t (&v)[4]) { v[0] = qf[i][0], v[1] = qf[i][1], v[2] = qf[i][2], v[3] = qf[i][3]; };
-            scores<DH>(a.k_codes + row * C::CODE, a.k_scales + row * C::NG, qget, g, t, x);
-            float mine = 0.f; // lane (g, t): key 8 (g / 2) + t + 4 (g % 2)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float p = ex2_approx(fmaf(x[n][e], f0, -z0)) + ex2_approx(fmaf(x[n][2 + e], f1, -z1));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) p += __shfl_xor_sync(0xffffffffu, p, d);
-                    if (g == 2 * n + e) mine = p;
-                }
-            const int key = 8 * (g >> 1) + t + 4 * (g & 1);
-            if (key < nk) {
+        auto qget = [&](int i, uint32_t (&v)[4]) { v[0] = qf[i][0], v[1] = qf[i][1], v[2] = qf[i][2], v[3] = qf[i][3]; };
+        const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
+        const int my_key = 8 * (g >> 1) + t + 4 * (g & 1);
+        // the next tile of this warp with visible keys: its rows and the lane's old weight are loaded one tile ahead
+        int next = 4 * cons.pos + warp;
+        struct Ahead {
+            KTile<DH> k;
+            int64_t row; // first row, -1: none
+            int nk;
+            float old;
+        } ahead;
+        auto fetch = [&] {
+            ahead.row = -1;
+            for (; next < 4 * cons.end && ahead.row < 0; next += kWThreads / 32) {
+                const int blk = w.key0(cons.b, cons.r, next / 4 - cons.seg, cons.len), key0 = blk + kTile * (next & 3);
+                ahead.nk = min(kTile, cons.len - key0);
+                if (blk < 0 || ahead.nk <= 0) continue;
+                ahead.row = row0 + key0;
+                ahead.k.load(a.k_codes + ahead.row * C::CODE, a.k_scales + ahead.row * C::NG, g, t);
                 // given blocks: kv4_decay_kernel has written decay * w_in to every visible key
-                const float old = GIVEN ? a.w_out[row + key] : (a.w_in ? a.decay * a.w_in[row + key] : 0.f);
-                a.w_out[row + key] = old + mine;
+                ahead.old = my_key >= ahead.nk ? 0.f : (GIVEN ? a.w_out[ahead.row + my_key] : (a.w_in ? a.decay * a.w_in[ahead.row + my_key] : 0.f));
             }
+        };
+        fetch();
+        while (ahead.row >= 0) {
+            const Ahead now = ahead;
+            fetch();
+            float x[4][4];
+            scores<DH>(now.k, qget, x);
+            // the heads' weights of key v = 2 n + e (the lane's columns): summed over the lanes g, which end with key g
+            float p[8];
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                p[v] = ex2_approx(fmaf(x[v >> 1][v & 1], f0, -z0)) + ex2_approx(fmaf(x[v >> 1][2 + (v & 1)], f1, -z1));
+#pragma unroll
+            for (int half = 4; half > 0; half >>= 1) {
+                const bool up = g & half;
+#pragma unroll
+                for (int v = 0; v < half; ++v) {
+                    const float give = up ? p[v] : p[v + half], keep = up ? p[v + half] : p[v];
+                    p[v] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+                }
+            }
+            if (my_key < now.nk) a.w_out[now.row + my_key] = now.old + p[0];
         }
     }
 }

@@ -4,16 +4,29 @@
 // others are kept, `keep` in all (equal weights: the lower position), in their order, and their rows
 // (codes, scales, index keys, weights) are copied to the front of another cache.
 //
-//   select : one CTA per (sequence, KV head) finds the weight of the last token that is kept, bit by
-//            bit on order-preserving integers, and writes the kept positions in order;
-//   move   : one warp per kept row copies it.
+//   select : a cluster of CTAs per (sequence, KV head), each with a contiguous part of the tokens,
+//            finds the weight of the last token kept by a radix select (three digits of order-preserving
+//            integers, most significant first, histograms in shared memory summed over the cluster),
+//            then writes the kept positions in order: every warp counts in a contiguous run, the counts
+//            are scanned over warps and CTAs, and a second walk writes. No atomics decide an order.
+//   move   : CTAs of 64 kept rows; a thread starts all its loads before its stores.
+#include <cooperative_groups.h>
+
 #include "kv4.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace msa {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kDigits = 3;
+constexpr int kBins = 2048, kCopies = 4; // copies of the histogram: attention weights crowd into few bins
+constexpr int kMaxCluster = 8;           // the portable limit
+
+__device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : (d == 1 ? 10 : 0); }
+__device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 
 // Integers that order like the weights (-0 and +0 are one value).
 __device__ __forceinline__ uint32_t weight_key(float w)
@@ -22,101 +35,224 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ int block_sum(int x, int* tmp)
-{
-    x = __reduce_add_sync(0xffffffffu, x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = x;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, tmp[threadIdx.x & 31]);
-}
+struct SelShared {
+    int hist[kBins * kCopies];
+    int sums[kBins];      // of the CTA's copies, read by the cluster
+    int tmp[kSelWarps];
+    uint32_t prefix;      // of the key looked for, and how many of its equals are still to be taken
+    int need;
+    int ties[kSelWarps], takes[kSelWarps];
+    int cta_ties, cta_sure; // this CTA's equal keys, and tokens kept without a choice
+};
 
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
 {
-    __shared__ int tmp[32], tmp2[32];
-    const int b = blockIdx.y, r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    extern __shared__ __align__(16) uint8_t sel_smem[];
+    SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), size = cluster.num_blocks();
+    const int seg = blockIdx.x / size, b = seg / a.H_kv; // (sequence, KV head)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = a.lens[b];
     const bool bad = len < 0 || len > a.L_max;
     const int n = bad ? 0 : len, left = min(n, a.keep);
-    int32_t* kept = a.kept + ((int64_t)b * a.H_kv + r) * a.keep;
-    if (tid == 0 && r == 0) {
+    int32_t* kept = a.kept + (int64_t)seg * a.keep;
+    if (tid == 0 && rank == 0 && seg % a.H_kv == 0) {
         if (bad) report_error(a.err, MSA_ERR_DEVICE_CHECK, 200 + b);
         a.lens_to[b] = left;
     }
-    for (int j = tid; j < a.keep; j += kSelThreads)
-        if (n <= a.keep) kept[j] = j < n ? j : -1;
-    if (n <= a.keep) return;
-    const float* w = a.w + ((int64_t)b * a.H_kv + r) * a.L_max;
-    const int c0 = a.first, c1 = n - a.recent, need = a.keep - a.first - a.recent; // candidates [c0, c1)
-    uint32_t T = 0; // the need-th largest key
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t cand = T | (1u << bit);
-        int cnt = 0;
-        for (int j = c0 + tid; j < c1; j += kSelThreads) cnt += weight_key(w[j]) >= cand;
-        if (block_sum(cnt, tmp) >= need) T = cand;
+    if (n <= a.keep) { // the whole cluster
+        for (int j = rank * kSelThreads + tid; j < a.keep; j += size * kSelThreads) kept[j] = j < n ? j : -1;
+        return;
     }
-    int above = 0;
-    for (int j = c0 + tid; j < c1; j += kSelThreads) above += weight_key(w[j]) > T;
-    int ties = need - block_sum(above, tmp); // equal weights still to take, in order
-    if (need == 0) ties = 0;
-    int base = 0;
-    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const bool in = j < n, mid = in && j >= c0 && j < c1;
-        const uint32_t key = mid ? weight_key(w[j]) : 0u;
-        const bool tie = mid && key == T && need > 0;
-        const unsigned tb = __ballot_sync(0xffffffffu, tie);
-        __syncthreads();
-        if (lane == 0) tmp[warp] = __popc(tb);
-        __syncthreads();
-        int before = 0, all = 0;
-        for (int i = 0; i < 32; ++i) {
-            before += i < warp ? tmp[i] : 0;
-            all += tmp[i];
+    const float* w = a.w + (int64_t)seg * a.L_max;
+    const int c0 = a.first, c1 = n - a.recent; // candidates
+    // this CTA's tokens, in runs of whole warps' steps
+    const int per = (n + size * kSelThreads - 1) / (size * kSelThreads) * kSelThreads;
+    const int lo = min(n, rank * per), hi = min(n, lo + per);
+    uint32_t T = 0xFFFFFFFFu; // no key is above it
+    int need = a.keep - a.first - a.recent;
+    if (need > 0) {
+        T = 0;
+        for (int d = 0; d < kDigits; ++d) {
+            for (int i = tid; i < kBins * kCopies; i += kSelThreads) sh.hist[i] = 0;
+            __syncthreads();
+            const int shift = digit_shift(d), bits = digit_bits(d);
+            const uint32_t above = d == 0 ? 0u : 0xFFFFFFFFu << (shift + bits);
+#pragma unroll 8
+            for (int j = max(lo, c0) + tid; j < min(hi, c1); j += kSelThreads) {
+                const uint32_t key = weight_key(w[j]);
+                if ((key & above) == T)
+                    atomicAdd(&sh.hist[((key >> shift) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
+            }
+            __syncthreads();
+            for (int i = tid; i < kBins; i += kSelThreads) {
+                const int4 h = *reinterpret_cast<const int4*>(&sh.hist[i * kCopies]);
+                sh.sums[i] = h.x + h.y + h.z + h.w;
+            }
+            cluster.sync();
+            // bins in descending order, two to a thread: the one where the counts reach `need`
+            int x[2], mine = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int bin = kBins - 1 - (2 * tid + u);
+                x[u] = 0;
+                for (int r = 0; r < size; ++r) x[u] += cluster.map_shared_rank(sh.sums, r)[bin];
+                mine += x[u];
+            }
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (lane == 31) sh.tmp[warp] = incl;
+            __syncthreads();
+            int before = incl - mine;
+            for (int i = 0; i < warp; ++i) before += sh.tmp[i];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (before < need && before + x[u] >= need) { // one bin of one thread
+                    sh.prefix = T | ((uint32_t)(kBins - 1 - (2 * tid + u)) << shift);
+                    sh.need = need - before;
+                }
+                before += x[u];
+            }
+            cluster.sync(); // the cluster has read this CTA's sums
+            T = sh.prefix;
+            need = sh.need;
         }
-        const bool take = in && (!mid || (need > 0 && (key > T || (tie && before + __popc(tb & ((1u << lane) - 1u)) < ties))));
-        ties -= min(ties, all);
+    }
+    // ---------------------------------------------------------------- kept positions in order
+    // a token stays without a choice (outside the candidates, or above T), or as one of the first `need`
+    // equal to T; a warp's run is contiguous
+    const int run = per / kSelWarps, r0 = min(hi, lo + warp * run), r1 = min(hi, r0 + run);
+    auto sure = [&](int j, uint32_t& key) {
+        const bool mid = j >= c0 && j < c1;
+        key = mid ? weight_key(w[j]) : 0u;
+        return !mid || key > T;
+    };
+    const bool choose = a.keep - a.first - a.recent > 0;
+    int n_sure = 0, n_tie = 0;
+#pragma unroll 4
+    for (int j = r0 + lane; j < r1; j += 32) {
+        uint32_t key;
+        const bool s = sure(j, key);
+        n_sure += s;
+        n_tie += !s && choose && key == T;
+    }
+    n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+    n_tie = __reduce_add_sync(0xffffffffu, n_tie);
+    if (lane == 0) {
+        sh.takes[warp] = n_sure;
+        sh.ties[warp] = n_tie;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int s = __reduce_add_sync(0xffffffffu, sh.takes[lane]), t = __reduce_add_sync(0xffffffffu, sh.ties[lane]);
+        if (lane == 0) {
+            sh.cta_sure = s;
+            sh.cta_ties = t;
+        }
+    }
+    cluster.sync();
+    int at = 0, ties = 0; // kept without a choice, and equal keys, before this warp's run
+    for (int r = 0; r < rank; ++r) {
+        at += *cluster.map_shared_rank(&sh.cta_sure, r);
+        ties += *cluster.map_shared_rank(&sh.cta_ties, r);
+    }
+    for (int i = 0; i < warp; ++i) {
+        at += sh.takes[i];
+        ties += sh.ties[i];
+    }
+    at += min(ties, need);
+    for (int j0 = r0; j0 < r1; j0 += 32) {
+        const int j = j0 + lane;
+        uint32_t key = 0;
+        const bool s = j < r1 && sure(j, key);
+        const bool tie = j < r1 && !s && choose && key == T;
+        const unsigned tb = __ballot_sync(0xffffffffu, tie), below = (1u << lane) - 1u;
+        const bool take = s || (tie && ties + __popc(tb & below) < need);
         const unsigned kb = __ballot_sync(0xffffffffu, take);
-        if (lane == 0) tmp2[warp] = __popc(kb);
-        __syncthreads();
-        before = 0;
-        all = 0;
-        for (int i = 0; i < 32; ++i) {
-            before += i < warp ? tmp2[i] : 0;
-            all += tmp2[i];
-        }
-        const int at = base + before + __popc(kb & ((1u << lane) - 1u));
-        if (take && at < a.keep) kept[at] = j;
-        base += all;
+        if (take) kept[at + __popc(kb & below)] = j;
+        at += __popc(kb);
+        ties += __popc(tb);
     }
+    cluster.sync(); // the cluster has read this CTA's counts
 }
 
-__global__ void __launch_bounds__(256) kv4_move_kernel(Kv4EvictArgs a)
+constexpr int kMoveRows = 64, kMoveThreads = 256;
+
+template <int DH>
+__global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4EvictArgs a)
 {
-    const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31;
-    const int left = a.lens_to[b];
-    const int32_t* kept = a.kept + ((int64_t)b * a.H_kv + r) * a.keep;
-    const int64_t from0 = ((int64_t)b * a.H_kv + r) * a.L_max, to0 = ((int64_t)b * a.H_kv + r) * a.L_to;
-    const int cu = a.d_h / 32, iu = a.k_idx ? a.d_idx / 8 : 0, sb = a.d_h / 16; // 16-byte units; bytes of scales
-    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < left; i += gridDim.x * 8) {
-        const int j = kept[i];
-        const int64_t from = from0 + j, to = to0 + i;
-        int u = lane;
-        if (u < cu) {
-            reinterpret_cast<uint4*>(a.k_codes_to)[to * cu + u] = reinterpret_cast<const uint4*>(a.k_codes)[from * cu + u];
-        } else if ((u -= cu) < cu) {
-            reinterpret_cast<uint4*>(a.v_codes_to)[to * cu + u] = reinterpret_cast<const uint4*>(a.v_codes)[from * cu + u];
-        } else if ((u -= cu) < sb / 4) {
-            reinterpret_cast<uint32_t*>(a.k_scales_to)[to * (sb / 4) + u] = reinterpret_cast<const uint32_t*>(a.k_scales)[from * (sb / 4) + u];
-        } else if ((u -= sb / 4) < sb / 4) {
-            reinterpret_cast<uint32_t*>(a.v_scales_to)[to * (sb / 4) + u] = reinterpret_cast<const uint32_t*>(a.v_scales)[from * (sb / 4) + u];
-        } else if ((u -= sb / 4) == 0 && a.w_to) {
-            a.w_to[to] = a.w[from];
+    constexpr int CU = DH / 32, SW = DH / 64;                         // 16-byte units of codes, words of scales per row
+    constexpr int CN = kMoveRows * CU / kMoveThreads > 0 ? kMoveRows * CU / kMoveThreads : 1;
+    constexpr int IN = kMoveRows * 16 / kMoveThreads;                 // index keys: at most 16 units per row
+    __shared__ int src[kMoveRows];
+    const int b = blockIdx.z, r = blockIdx.y, tid = threadIdx.x, i0 = blockIdx.x * kMoveRows;
+    const int rows = min(kMoveRows, a.lens_to[b] - i0);
+    if (rows <= 0) return;
+    const int64_t seg = (int64_t)b * a.H_kv + r;
+    if (tid < rows) src[tid] = a.kept[seg * a.keep + i0 + tid];
+    __syncthreads();
+    const int64_t from0 = seg * a.L_max, to0 = seg * a.L_to + i0;
+    const uint4 *kc = reinterpret_cast<const uint4*>(a.k_codes) + from0 * CU, *vc = reinterpret_cast<const uint4*>(a.v_codes) + from0 * CU;
+    const uint4* ki = reinterpret_cast<const uint4*>(a.k_idx);
+    const int iu = a.k_idx ? a.d_idx / 8 : 0;
+    uint4 xk[CN], xv[CN], xi[IN];
+    uint32_t xs = 0;
+#pragma unroll
+    for (int n = 0; n < CN; ++n) {
+        const int u = n * kMoveThreads + tid, i = u / CU;
+        if (i < rows) {
+            const int64_t p = (int64_t)src[i] * CU + u % CU;
+            xk[n] = kc[p];
+            xv[n] = vc[p];
         }
-        if (lane >= 32 - iu) { // the last lanes: at most 16 units, which the others leave free
-            u = lane - (32 - iu);
-            reinterpret_cast<uint4*>(a.k_idx_to)[(((int64_t)b * a.L_to + i) * a.H_kv + r) * iu + u] =
-                reinterpret_cast<const uint4*>(a.k_idx)[(((int64_t)b * a.L_max + j) * a.H_kv + r) * iu + u];
+    }
+#pragma unroll
+    for (int n = 0; n < IN; ++n) {
+        const int u = n * kMoveThreads + tid;
+        if (u < rows * iu) {
+            const int i = u / iu;
+            xi[n] = ki[(((int64_t)b * a.L_max + src[i]) * a.H_kv + r) * iu + u % iu];
+        }
+    }
+    // scales of K, of V (a word each at d_h = 64, two at 128) and the weight: a quarter of the threads each
+    const int part = tid / kMoveRows, i = tid % kMoveRows;
+    uint32_t xs2 = 0;
+    if (i < rows) {
+        const int64_t p = from0 + src[i];
+        if (part < 2) {
+            const uint32_t* s = reinterpret_cast<const uint32_t*>(part == 0 ? a.k_scales : a.v_scales) + p * SW;
+            xs = s[0];
+            if (SW == 2) xs2 = s[SW - 1];
+        } else if (part == 2 && a.w_to) {
+            xs = __float_as_uint(a.w[p]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < CN; ++n) {
+        const int u = n * kMoveThreads + tid;
+        if (u / CU < rows) {
+            reinterpret_cast<uint4*>(a.k_codes_to)[to0 * CU + u] = xk[n];
+            reinterpret_cast<uint4*>(a.v_codes_to)[to0 * CU + u] = xv[n];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < IN; ++n) {
+        const int u = n * kMoveThreads + tid;
+        if (u < rows * iu)
+            reinterpret_cast<uint4*>(a.k_idx_to)[(((int64_t)b * a.L_to + i0 + u / iu) * a.H_kv + r) * iu + u % iu] = xi[n];
+    }
+    if (i < rows) {
+        if (part < 2) {
+            uint32_t* s = reinterpret_cast<uint32_t*>(part == 0 ? a.k_scales_to : a.v_scales_to) + (to0 + i) * SW;
+            s[0] = xs;
+            if (SW == 2) s[SW - 1] = xs2;
+        } else if (part == 2 && a.w_to) {
+            a.w_to[to0 + i] = __uint_as_float(xs);
         }
     }
 }
@@ -125,10 +261,29 @@ __global__ void __launch_bounds__(256) kv4_move_kernel(Kv4EvictArgs a)
 
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s)
 {
+    cudaError_t e = cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelShared));
+    if (e != cudaSuccess) return e;
+    // a CTA for every 8192 tokens a cache may hold
+    int size = 1;
+    while (size < kMaxCluster && (int64_t)size * 8192 < a.L_max) size *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * size));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = sizeof(SelShared);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)size, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     trace_begin(s);
-    kv4_select_kernel<<<dim3(a.H_kv, a.B), kSelThreads, 0, s>>>(a);
-    const int gx = (a.keep + 31) / 32; // 4 rows per warp
-    kv4_move_kernel<<<dim3(gx, a.H_kv, a.B), 256, 0, s>>>(a);
+    e = cudaLaunchKernelEx(&cfg, kv4_select_kernel, a);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((a.keep + kMoveRows - 1) / kMoveRows, a.H_kv, a.B);
+    if (a.d_h == 128)
+        kv4_move_kernel<128><<<grid, kMoveThreads, 0, s>>>(a);
+    else
+        kv4_move_kernel<64><<<grid, kMoveThreads, 0, s>>>(a);
     trace_end(s, MSA_KERNEL_KV4_EVICT);
     note_launch(2);
     return cudaGetLastError();

@@ -1054,6 +1054,7 @@ static Kv4RowsArgs kv4_rows_args(const msa_kv4_cache* c, int64_t T, const int32_
     a.scales[1] = c->v_scales;
     a.t[0] = c->k_scale;
     a.t[1] = c->v_scale;
+    for (int i = 0; i < 2; ++i) a.rt[i] = a.t[i] >= 0x1p-20f && a.t[i] <= 0x1p20f ? 1.f / a.t[i] : 0.f;
     a.starts = starts;
     a.cu = cu;
     a.T = T;
