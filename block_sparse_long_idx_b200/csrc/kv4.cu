@@ -3,9 +3,9 @@
 // append: for every 16 elements x of a new row
 //   y = fl32(x / t), a = max |y|, s = E4M3(min(fl32(a / 6), 448)), code = E2M1(fl32(y / s))
 // with all roundings to nearest even and codes saturating at 6; s = 0 gives zero codes. read: the
-// values code * s * t rounded to bf16. One thread per 16 elements of K and of V, CTAs of one head's consecutive
-// rows, so that the head-major cache side is written (read) in whole contiguous runs and the
-// token-major side in whole rows of d_h elements.
+// values code * s * t rounded to bf16. CTAs take one head's consecutive rows of K and of V, so that the
+// head-major cache side is written (read) in whole contiguous runs and the token-major side in whole
+// rows of d_h elements; the rows' places are looked up once per CTA.
 #include "kv4.cuh"
 
 namespace msa {
@@ -13,10 +13,17 @@ namespace msa {
 namespace {
 
 constexpr int kRowThreads = 256;
+#ifndef AST
+#define AST 1
+#define RST 4
+#endif
+constexpr int kAppendSteps = AST, kReadSteps = RST; // row steps of a CTA where there are rows enough for every SM
 
-// Sequence and cache position of packed row i; false (reported) when the batch tables do not place it.
-__device__ __forceinline__ bool locate_row(const Kv4RowsArgs& a, int64_t i, int& b, int64_t& pos)
+// Cache row (counting rows of all sequences and heads, for head 0) of packed row i; -1 (reported) when the
+// batch tables do not place it.
+__device__ __forceinline__ int64_t locate_row(const Kv4RowsArgs& a, int64_t i)
 {
+    int b = (int)i; // without tables T = B
     int64_t off = 0;
     if (a.cu) {
         int lo = 0, hi = a.B - 1; // the last b with cu[b] <= i
@@ -28,25 +35,31 @@ __device__ __forceinline__ bool locate_row(const Kv4RowsArgs& a, int64_t i, int&
         off = i - a.cu[b];
         if (off < 0 || i >= a.cu[b + 1]) {
             report_error(a.err, MSA_ERR_DEVICE_CHECK, 300);
-            return false;
+            return -1;
         }
-    } else {
-        b = (int)i; // T = B
     }
-    pos = (int64_t)a.starts[b] + off;
-    if (a.starts[b] < 0 || pos >= a.L_max) {
+    const int start = a.starts[b];
+    if (start < 0 || start + off >= a.L_max) {
         report_error(a.err, MSA_ERR_DEVICE_CHECK, 301);
-        return false;
+        return -1;
     }
-    return true;
+    return (int64_t)b * a.H_kv * a.L_max + start + off;
 }
 
-// Correctly rounded x / d from r = 1 / d correctly rounded (Markstein's correction of x * r by its exact
-// residual), for d > 0 and where nothing over- or underflows: see quantise16.
-__device__ __forceinline__ float quotient(float x, float d, float r)
+// The CTA's rows [i0, i0 + n): their cache rows in `place` (-1: none), by the first threads.
+__device__ __forceinline__ void locate_rows(const Kv4RowsArgs& a, int64_t i0, int n, int64_t* place)
 {
-    const float q = x * r;
-    return copysignf(fmaf(fmaf(-q, d, x), r, q), x); // the correction loses the sign of a zero
+    if (threadIdx.x < n) place[threadIdx.x] = i0 + threadIdx.x < a.T ? locate_row(a, i0 + threadIdx.x) : -1;
+    __syncthreads();
+}
+
+// Correctly rounded x / d, two at a time, from r = 1 / d correctly rounded (Markstein's correction of x * r
+// by its exact residual), for d > 0 and where nothing over- or underflows: see quantise16. A zero may lose
+// its sign.
+__device__ __forceinline__ uint64_t quotient2(uint64_t x, float d, float r)
+{
+    const uint64_t rr = f2_pack(r, r), q = f2_mul(x, rr), nq = q ^ 0x8000000080000000ull;
+    return f2_fma(f2_fma(nq, f2_pack(d, d), x), rr, q);
 }
 
 // The 16 elements of w as codes c and their scale's byte. rt = 1 / t, or 0 where t is outside [2^-20,
@@ -55,131 +68,146 @@ __device__ __forceinline__ float quotient(float x, float d, float r)
 // smallest code, and end as 0 either way.
 __device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], float t, float rt, uint32_t (&c)[2])
 {
-    float y[16], amax = 0.f;
+    uint32_t m = 0u; // largest |x|: bf16 magnitudes order like integers
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        y[2 * e] = bf16_lo(w[e]);
-        y[2 * e + 1] = bf16_hi(w[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(y[e]));
-    const bool plain = rt == 0.f || !(amax < 0x1p100f);
+    for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+    m = max(m >> 16, m & 0xFFFFu);
+    float amax = __uint_as_float(m << 16);
     c[0] = c[1] = 0u;
-    if (plain) {
-        amax = 0.f;
+    if (rt == 0.f || !(amax < 0x1p100f)) {
+        amax = __fdiv_rn(amax, t); // rounding keeps the order
+        const uint32_t s8 = e4m3x2_pack(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu;
+        if (s8 == 0) return 0u;
+        const float s = e4m3x2_unpack(s8).x;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            y[e] = __fdiv_rn(y[e], t);
-            amax = fmaxf(amax, fabsf(y[e]));
-        }
-    } else if (t != 1.f) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = quotient(y[e], t, rt);
-        amax = quotient(amax, t, rt); // rounding keeps the order
+        for (int e = 0; e < 8; ++e)
+            c[e >> 2] |= e2m1x2_pack(__fdiv_rn(__fdiv_rn(bf16_lo(w[e]), t), s), __fdiv_rn(__fdiv_rn(bf16_hi(w[e]), t), s)) << (8 * (e & 3));
+        return s8;
     }
+    if (t != 1.f) amax = f2_lo(quotient2(f2_pack(amax, 0.f), t, rt));
     const uint32_t s8 = e4m3x2_pack(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu;
     if (s8 == 0) return 0u;
-    const float s = e4m3x2_unpack(s8).x;
-    if (plain) {
+    const float s = e4m3x2_unpack(s8).x, rs = __frcp_rn(s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            c[e >> 2] |= e2m1x2_pack(__fdiv_rn(y[2 * e], s), __fdiv_rn(y[2 * e + 1], s)) << (8 * (e & 3));
-    } else {
-        const float rs = __frcp_rn(s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            c[e >> 2] |= e2m1x2_pack(quotient(y[2 * e], s, rs), quotient(y[2 * e + 1], s, rs)) << (8 * (e & 3));
+    for (int e = 0; e < 8; ++e) {
+        const float lo = bf16_lo(w[e]), hi = bf16_hi(w[e]);
+        uint64_t y = f2_pack(lo, hi);
+        if (t != 1.f) y = quotient2(y, t, rt);
+        const uint64_t q = quotient2(y, s, rs);
+        c[e >> 2] |= e2m1x2_pack(copysignf(f2_lo(q), lo), copysignf(f2_hi(q), hi)) << (8 * (e & 3));
     }
     return s8;
 }
 
-template <int DH>
+// A thread takes 16 elements of K and of V of one row per step.
+template <int DH, int STEPS>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowsArgs a)
 {
-    constexpr int NG = DH / 16, ROWS = kRowThreads / NG;
-    const int g = threadIdx.x % NG, r = blockIdx.y;
-    const int64_t i = (int64_t)blockIdx.x * ROWS + threadIdx.x / NG;
-    if (i >= a.T) return;
-    uint32_t w[2][8];
+    constexpr int NG = DH / 16, ROWS = kRowThreads / NG, N = ROWS * STEPS;
+    __shared__ int64_t place[N];
+    const int g = threadIdx.x % NG, i = threadIdx.x / NG, r = blockIdx.y;
+    const int64_t i0 = (int64_t)blockIdx.x * N;
+    uint32_t w[STEPS][2][8];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) { // the loads of both tensors, and of the tables, in flight together
-        const uint4* src = reinterpret_cast<const uint4*>(a.x[which] + i * a.x_stride[which] + (int64_t)r * DH + g * 16);
-        const uint4 v0 = src[0], v1 = src[1];
-        w[which][0] = v0.x, w[which][1] = v0.y, w[which][2] = v0.z, w[which][3] = v0.w;
-        w[which][4] = v1.x, w[which][5] = v1.y, w[which][6] = v1.z, w[which][7] = v1.w;
+    for (int u = 0; u < STEPS; ++u) { // in flight while the places are looked up
+        const int64_t row = i0 + u * ROWS + i;
+        if (row < a.T) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const uint4* src = reinterpret_cast<const uint4*>(a.x[which] + row * a.x_stride[which] + (int64_t)r * DH + g * 16);
+                const uint4 v0 = src[0], v1 = src[1];
+                uint32_t* x = w[u][which];
+                x[0] = v0.x, x[1] = v0.y, x[2] = v0.z, x[3] = v0.w, x[4] = v1.x, x[5] = v1.y, x[6] = v1.z, x[7] = v1.w;
+            }
+        }
     }
-    int b;
-    int64_t pos;
-    if (!locate_row(a, i, b, pos)) return;
-    const int64_t row = ((int64_t)b * a.H_kv + r) * a.L_max + pos;
+    locate_rows(a, i0, N, place);
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        uint32_t c[2];
-        const uint32_t s8 = quantise16(w[which], a.t[which], a.rt[which], c);
-        *reinterpret_cast<uint2*>(a.codes[which] + row * (DH / 2) + g * 8) = make_uint2(c[0], c[1]);
-        a.scales[which][row * NG + g] = (uint8_t)s8;
+    for (int u = 0; u < STEPS; ++u) {
+        if (place[u * ROWS + i] < 0) continue;
+        const int64_t row = place[u * ROWS + i] + r * a.L_max;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            uint32_t c[2];
+            const uint32_t s8 = quantise16(w[u][which], a.t[which], a.rt[which], c);
+            *reinterpret_cast<uint2*>(a.codes[which] + row * (DH / 2) + g * 8) = make_uint2(c[0], c[1]);
+            a.scales[which][row * NG + g] = (uint8_t)s8;
+        }
     }
 }
 
-template <int DH>
+// A thread takes 8 elements of K and of V of one row per step: 16-byte stores, whole rows to a warp's.
+template <int DH, int STEPS>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowsArgs a)
 {
-    constexpr int NG = DH / 16, ROWS = kRowThreads / NG;
-    const int g = threadIdx.x % NG, r = blockIdx.y;
-    const int64_t i = (int64_t)blockIdx.x * ROWS + threadIdx.x / NG;
-    int b;
-    int64_t pos;
-    if (i >= a.T || !locate_row(a, i, b, pos)) return;
-    const int64_t row = ((int64_t)b * a.H_kv + r) * a.L_max + pos;
-    uint2 c[2];
-    uint32_t s8[2];
+    constexpr int NU = DH / 8, ROWS = kRowThreads / NU, N = ROWS * STEPS;
+    __shared__ int64_t place[N];
+    const int e8 = threadIdx.x % NU, i = threadIdx.x / NU, r = blockIdx.y;
+    const int64_t i0 = (int64_t)blockIdx.x * N;
+    locate_rows(a, i0, N, place);
+    uint32_t c[STEPS][2], s8[STEPS][2];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        c[which] = *reinterpret_cast<const uint2*>(a.codes[which] + row * (DH / 2) + g * 8);
-        s8[which] = a.scales[which][row * NG + g];
+    for (int u = 0; u < STEPS; ++u) {
+        const int64_t row = place[u * ROWS + i] + r * a.L_max;
+        if (place[u * ROWS + i] < 0) continue;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            c[u][which] = *reinterpret_cast<const uint32_t*>(a.codes[which] + row * (DH / 2) + e8 * 4);
+            s8[u][which] = a.scales[which][row * (DH / 16) + e8 / 2];
+        }
     }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const float s = e4m3x2_unpack(s8[which]).x, t = a.t[which];
-        uint32_t h[2][4], o[8];
-        e2m1x8_to_f16x2(c[which].x, h[0]);
-        e2m1x8_to_f16x2(c[which].y, h[1]);
+    for (int u = 0; u < STEPS; ++u) {
+        if (place[u * ROWS + i] < 0) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 f = unpack_f16x2(h[e >> 2][e & 3]);
-            o[e] = pack_bf16x2(f.x * s * t, f.y * s * t); // code * s is exact
+        for (int which = 0; which < 2; ++which) {
+            const float s = e4m3x2_unpack(s8[u][which]).x, t = a.t[which];
+            uint32_t h[4], o[4];
+            e2m1x8_to_f16x2(c[u][which], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack_f16x2(h[e]);
+                o[e] = pack_bf16x2(f.x * s * t, f.y * s * t); // code * s is exact
+            }
+            *reinterpret_cast<uint4*>(a.y[which] + ((i0 + u * ROWS + i) * a.H_kv + r) * (int64_t)DH + e8 * 8) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        uint4* dst = reinterpret_cast<uint4*>(a.y[which] + (i * a.H_kv + r) * (int64_t)DH + g * 16);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
-dim3 rows_grid(const Kv4RowsArgs& a)
+template <int DH, int STEPS>
+struct Append {
+    static constexpr int ROWS = kRowThreads / (DH / 16) * STEPS;
+    static void run(const Kv4RowsArgs& a, dim3 grid, cudaStream_t s) { kv4_append_kernel<DH, STEPS><<<grid, kRowThreads, 0, s>>>(a); }
+};
+template <int DH, int STEPS>
+struct Read {
+    static constexpr int ROWS = kRowThreads / (DH / 8) * STEPS;
+    static void run(const Kv4RowsArgs& a, dim3 grid, cudaStream_t s) { kv4_read_kernel<DH, STEPS><<<grid, kRowThreads, 0, s>>>(a); }
+};
+
+// STEPS row steps to a CTA (more loads in flight) once that leaves two CTAs for every SM, else one.
+template <template <int, int> class K, int DH, int STEPS>
+void launch_rows(const Kv4RowsArgs& a, cudaStream_t s)
 {
-    const int rows = kRowThreads / (a.d_h / 16);
-    return dim3((unsigned)((a.T + rows - 1) / rows), a.H_kv);
+    const auto ctas = [&](int rows) { return (a.T + rows - 1) / rows; };
+    if (ctas(K<DH, STEPS>::ROWS) * a.H_kv >= 2 * kKv4Ctas)
+        K<DH, STEPS>::run(a, dim3((unsigned)ctas(K<DH, STEPS>::ROWS), a.H_kv), s);
+    else
+        K<DH, 1>::run(a, dim3((unsigned)ctas(K<DH, 1>::ROWS), a.H_kv), s);
+    note_launch(1);
 }
 
 } // namespace
 
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s)
 {
-    if (a.d_h == 128)
-        kv4_append_kernel<128><<<rows_grid(a), kRowThreads, 0, s>>>(a);
-    else
-        kv4_append_kernel<64><<<rows_grid(a), kRowThreads, 0, s>>>(a);
-    note_launch(1);
+    a.d_h == 128 ? launch_rows<Append, 128, kAppendSteps>(a, s) : launch_rows<Append, 64, kAppendSteps>(a, s);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s)
 {
-    if (a.d_h == 128)
-        kv4_read_kernel<128><<<rows_grid(a), kRowThreads, 0, s>>>(a);
-    else
-        kv4_read_kernel<64><<<rows_grid(a), kRowThreads, 0, s>>>(a);
-    note_launch(1);
+    a.d_h == 128 ? launch_rows<Read, 128, kReadSteps>(a, s) : launch_rows<Read, 64, kReadSteps>(a, s);
     return cudaGetLastError();
 }
 

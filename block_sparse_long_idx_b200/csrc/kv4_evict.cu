@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
             for (int u = 0; u < 2; ++u) {
                 const int bin = kBins - 1 - (2 * tid + u);
                 x[u] = 0;
-                for (int r = 0; r < size; ++r) x[u] += cluster.map_shared_rank(sh.sums, r)[bin];
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) // loads in flight together
+                    if (r < size) x[u] += cluster.map_shared_rank(sh.sums, r)[bin];
                 mine += x[u];
             }
             int incl = mine;
@@ -108,8 +110,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
             }
             if (lane == 31) sh.tmp[warp] = incl;
             __syncthreads();
-            int before = incl - mine;
-            for (int i = 0; i < warp; ++i) before += sh.tmp[i];
+            int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sh.tmp[lane] : 0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if (before < need && before + x[u] >= need) { // one bin of one thread
@@ -127,19 +128,32 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
     // a token stays without a choice (outside the candidates, or above T), or as one of the first `need`
     // equal to T; a warp's run is contiguous
     const int run = per / kSelWarps, r0 = min(hi, lo + warp * run), r1 = min(hi, r0 + run);
-    auto sure = [&](int j, uint32_t& key) {
-        const bool mid = j >= c0 && j < c1;
-        key = mid ? weight_key(w[j]) : 0u;
-        return !mid || key > T;
-    };
+    constexpr int kBatch = 8; // a lane's loads in flight
     const bool choose = a.keep - a.first - a.recent > 0;
+    uint32_t key[kBatch];
+    bool sure[kBatch], tie[kBatch];
+    auto classify = [&](int j0) { // tokens j0 + 32 i + lane
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = j0 + 32 * i + lane;
+            key[i] = j < r1 && j >= c0 && j < c1 ? weight_key(w[j]) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = j0 + 32 * i + lane;
+            const bool mid = j >= c0 && j < c1;
+            sure[i] = j < r1 && (!mid || key[i] > T);
+            tie[i] = j < r1 && mid && choose && key[i] == T;
+        }
+    };
     int n_sure = 0, n_tie = 0;
-#pragma unroll 4
-    for (int j = r0 + lane; j < r1; j += 32) {
-        uint32_t key;
-        const bool s = sure(j, key);
-        n_sure += s;
-        n_tie += !s && choose && key == T;
+    for (int j0 = r0; j0 < r1; j0 += 32 * kBatch) {
+        classify(j0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            n_sure += sure[i];
+            n_tie += tie[i];
+        }
     }
     n_sure = __reduce_add_sync(0xffffffffu, n_sure);
     n_tie = __reduce_add_sync(0xffffffffu, n_tie);
@@ -156,27 +170,27 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
         }
     }
     cluster.sync();
-    int at = 0, ties = 0; // kept without a choice, and equal keys, before this warp's run
-    for (int r = 0; r < rank; ++r) {
-        at += *cluster.map_shared_rank(&sh.cta_sure, r);
-        ties += *cluster.map_shared_rank(&sh.cta_ties, r);
+    // kept without a choice, and equal keys, before this warp's run: of the CTAs and of the warps before
+    int at = lane < warp ? sh.takes[lane] : 0, ties = lane < warp ? sh.ties[lane] : 0;
+    if (lane < rank) {
+        at += *cluster.map_shared_rank(&sh.cta_sure, lane);
+        ties += *cluster.map_shared_rank(&sh.cta_ties, lane);
     }
-    for (int i = 0; i < warp; ++i) {
-        at += sh.takes[i];
-        ties += sh.ties[i];
-    }
+    at = __reduce_add_sync(0xffffffffu, at);
+    ties = __reduce_add_sync(0xffffffffu, ties);
     at += min(ties, need);
-    for (int j0 = r0; j0 < r1; j0 += 32) {
-        const int j = j0 + lane;
-        uint32_t key = 0;
-        const bool s = j < r1 && sure(j, key);
-        const bool tie = j < r1 && !s && choose && key == T;
-        const unsigned tb = __ballot_sync(0xffffffffu, tie), below = (1u << lane) - 1u;
-        const bool take = s || (tie && ties + __popc(tb & below) < need);
-        const unsigned kb = __ballot_sync(0xffffffffu, take);
-        if (take) kept[at + __popc(kb & below)] = j;
-        at += __popc(kb);
-        ties += __popc(tb);
+    const unsigned below = (1u << lane) - 1u;
+    for (int j0 = r0; j0 < r1; j0 += 32 * kBatch) {
+        classify(j0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const unsigned tb = __ballot_sync(0xffffffffu, tie[i]);
+            const bool take = sure[i] || (tie[i] && ties + __popc(tb & below) < need);
+            const unsigned kb = __ballot_sync(0xffffffffu, take);
+            if (take) kept[at + __popc(kb & below)] = j0 + 32 * i + lane;
+            at += __popc(kb);
+            ties += __popc(tb);
+        }
     }
     cluster.sync(); // the cluster has read this CTA's counts
 }
