@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowsArgs a)
 {
     constexpr int NG = DH / 16, ROWS = kRowThreads / NG, N = ROWS * STEPS;
     __shared__ int64_t place[N];
-    const int g = threadIdx.x % NG, i = threadIdx.x / NG, r = blockIdx.y;
-    const int64_t i0 = (int64_t)blockIdx.x * N;
+    const int g = threadIdx.x % NG, i = threadIdx.x / NG, r = blockIdx.x % a.H_kv;
+    const int64_t i0 = (int64_t)(blockIdx.x / a.H_kv) * N;
     uint32_t w[STEPS][2][8];
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) { // in flight while the places are looked up
@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowsArgs a)
 {
     constexpr int NU = DH / 8, ROWS = kRowThreads / NU, N = ROWS * STEPS;
     __shared__ int64_t place[N];
-    const int e8 = threadIdx.x % NU, i = threadIdx.x / NU, r = blockIdx.y;
-    const int64_t i0 = (int64_t)blockIdx.x * N;
+    const int e8 = threadIdx.x % NU, i = threadIdx.x / NU, r = blockIdx.x % a.H_kv; // the heads of a row run together
+    const int64_t i0 = (int64_t)(blockIdx.x / a.H_kv) * N;
     locate_rows(a, i0, N, place);
     uint32_t c[STEPS][2], s8[STEPS][2];
 #pragma unroll
@@ -191,9 +191,9 @@ void launch_rows(const Kv4RowsArgs& a, cudaStream_t s)
 {
     const auto ctas = [&](int rows) { return (a.T + rows - 1) / rows; };
     if (ctas(K<DH, STEPS>::ROWS) * a.H_kv >= 2 * kKv4Ctas)
-        K<DH, STEPS>::run(a, dim3((unsigned)ctas(K<DH, STEPS>::ROWS), a.H_kv), s);
+        K<DH, STEPS>::run(a, dim3((unsigned)(ctas(K<DH, STEPS>::ROWS) * a.H_kv)), s);
     else
-        K<DH, 1>::run(a, dim3((unsigned)ctas(K<DH, 1>::ROWS), a.H_kv), s);
+        K<DH, 1>::run(a, dim3((unsigned)(ctas(K<DH, 1>::ROWS) * a.H_kv)), s);
     note_launch(1);
 }
 

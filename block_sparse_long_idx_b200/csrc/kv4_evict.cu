@@ -20,9 +20,9 @@ namespace msa {
 
 namespace {
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kDigits = 3;
-constexpr int kBins = 2048, kCopies = 4; // copies of the histogram: attention weights crowd into few bins
+constexpr int kBins = 2048, kCopies = 4; // copies of a histogram: attention weights crowd into few bins
 constexpr int kMaxCluster = 8;           // the portable limit
 
 __device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : (d == 1 ? 10 : 0); }
@@ -36,15 +36,18 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 }
 
 struct SelShared {
-    int hist[kBins * kCopies];
-    int sums[kBins];      // of the CTA's copies, read by the cluster
+    int hist[kDigits][kBins * kCopies];
+    int sums[2][kBins]; // of the CTA's copies, read by the cluster: digits alternate, so one barrier each is enough
     int tmp[kSelWarps];
-    uint32_t prefix;      // of the key looked for, and how many of its equals are still to be taken
+    uint32_t prefix; // of the key looked for, and how many of its equals are still to be taken
     int need;
     int ties[kSelWarps], takes[kSelWarps];
     int cta_ties, cta_sure; // this CTA's equal keys, and tokens kept without a choice
 };
 
+// Every warp owns a contiguous run of tokens, walked in rounds of 32 * KEYS. RESIDENT: the run is one round,
+// whose keys are read from memory once and stay in registers.
+template <int KEYS, bool RESIDENT>
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
 {
     extern __shared__ __align__(16) uint8_t sel_smem[];
@@ -67,41 +70,57 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
     }
     const float* w = a.w + (int64_t)seg * a.L_max;
     const int c0 = a.first, c1 = n - a.recent; // candidates
-    // this CTA's tokens, in runs of whole warps' steps
-    const int per = (n + size * kSelThreads - 1) / (size * kSelThreads) * kSelThreads;
-    const int lo = min(n, rank * per), hi = min(n, lo + per);
+    constexpr int kRound = 32 * KEYS;
+    const int run = RESIDENT ? kRound : (n + size * kSelWarps * kRound - 1) / (size * kSelWarps * kRound) * kRound;
+    const int r0 = min(n, (rank * kSelWarps + warp) * run), r1 = min(n, r0 + run);
+    uint32_t key[KEYS];
+    auto load = [&](int j0) { // keys of tokens j0 + 32 i + lane, 0 for those that are no candidates
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+            const int j = j0 + 32 * i + lane;
+            key[i] = j < r1 && j >= c0 && j < c1 ? weight_key(w[j]) : 0u;
+        }
+    };
+    auto is_mid = [&](int j) { return j < r1 && j >= c0 && j < c1; };
+    if (RESIDENT) load(r0);
     uint32_t T = 0xFFFFFFFFu; // no key is above it
     int need = a.keep - a.first - a.recent;
-    if (need > 0) {
+    const bool choose = need > 0;
+    if (choose) {
+        for (int i = tid; i < kDigits * kBins * kCopies / 4; i += kSelThreads)
+            reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
         T = 0;
         for (int d = 0; d < kDigits; ++d) {
-            for (int i = tid; i < kBins * kCopies; i += kSelThreads) sh.hist[i] = 0;
-            __syncthreads();
             const int shift = digit_shift(d), bits = digit_bits(d);
             const uint32_t above = d == 0 ? 0u : 0xFFFFFFFFu << (shift + bits);
-#pragma unroll 8
-            for (int j = max(lo, c0) + tid; j < min(hi, c1); j += kSelThreads) {
-                const uint32_t key = weight_key(w[j]);
-                if ((key & above) == T)
-                    atomicAdd(&sh.hist[((key >> shift) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
+            for (int j0 = r0; j0 < r1; j0 += kRound) {
+                if (!RESIDENT) load(j0);
+#pragma unroll
+                for (int i = 0; i < KEYS; ++i)
+                    if (is_mid(j0 + 32 * i + lane) && (key[i] & above) == T)
+                        atomicAdd(&sh.hist[d][((key[i] >> shift) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
             }
             __syncthreads();
+            int* sums = sh.sums[d & 1];
             for (int i = tid; i < kBins; i += kSelThreads) {
-                const int4 h = *reinterpret_cast<const int4*>(&sh.hist[i * kCopies]);
-                sh.sums[i] = h.x + h.y + h.z + h.w;
+                const int4 h = *reinterpret_cast<const int4*>(&sh.hist[d][i * kCopies]);
+                sums[i] = h.x + h.y + h.z + h.w;
             }
             cluster.sync();
-            // bins in descending order, two to a thread: the one where the counts reach `need`
-            int x[2], mine = 0;
+            // bins in descending order, four to a thread: the one where the counts reach `need`
+            constexpr int PER = kBins / kSelThreads;
+            static_assert(PER == 4, "a thread's bins are one 16-byte read");
+            const int top = kBins - PER * (tid + 1); // bins top + 3 .. top
+            int4 x = make_int4(0, 0, 0, 0);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int bin = kBins - 1 - (2 * tid + u);
-                x[u] = 0;
-#pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r) // loads in flight together
-                    if (r < size) x[u] += cluster.map_shared_rank(sh.sums, r)[bin];
-                mine += x[u];
+            for (int r = 0; r < kMaxCluster; ++r) { // loads in flight together
+                if (r < size) {
+                    const int4 y = *reinterpret_cast<const int4*>(cluster.map_shared_rank(sums, r) + top);
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
             }
+            const int mine = x.x + x.y + x.z + x.w;
             int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -111,48 +130,30 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
             if (lane == 31) sh.tmp[warp] = incl;
             __syncthreads();
             int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sh.tmp[lane] : 0);
+            const int count[PER] = {x.w, x.z, x.y, x.x};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (before < need && before + x[u] >= need) { // one bin of one thread
-                    sh.prefix = T | ((uint32_t)(kBins - 1 - (2 * tid + u)) << shift);
+            for (int u = 0; u < PER; ++u) {
+                if (before < need && before + count[u] >= need) { // one bin of one thread
+                    sh.prefix = T | ((uint32_t)(top + PER - 1 - u) << shift);
                     sh.need = need - before;
                 }
-                before += x[u];
+                before += count[u];
             }
-            cluster.sync(); // the cluster has read this CTA's sums
+            __syncthreads();
             T = sh.prefix;
             need = sh.need;
         }
     }
     // ---------------------------------------------------------------- kept positions in order
-    // a token stays without a choice (outside the candidates, or above T), or as one of the first `need`
-    // equal to T; a warp's run is contiguous
-    const int run = per / kSelWarps, r0 = min(hi, lo + warp * run), r1 = min(hi, r0 + run);
-    constexpr int kBatch = 8; // a lane's loads in flight
-    const bool choose = a.keep - a.first - a.recent > 0;
-    uint32_t key[kBatch];
-    bool sure[kBatch], tie[kBatch];
-    auto classify = [&](int j0) { // tokens j0 + 32 i + lane
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int j = j0 + 32 * i + lane;
-            key[i] = j < r1 && j >= c0 && j < c1 ? weight_key(w[j]) : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int j = j0 + 32 * i + lane;
-            const bool mid = j >= c0 && j < c1;
-            sure[i] = j < r1 && (!mid || key[i] > T);
-            tie[i] = j < r1 && mid && choose && key[i] == T;
-        }
-    };
+    // a token stays without a choice (not a candidate, or above T), or as one of the first `need` equal to T
     int n_sure = 0, n_tie = 0;
-    for (int j0 = r0; j0 < r1; j0 += 32 * kBatch) {
-        classify(j0);
+    for (int j0 = r0; j0 < r1; j0 += kRound) {
+        if (!RESIDENT) load(j0);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            n_sure += sure[i];
-            n_tie += tie[i];
+        for (int i = 0; i < KEYS; ++i) {
+            const int j = j0 + 32 * i + lane;
+            n_sure += j < r1 && (!is_mid(j) || key[i] > T);
+            n_tie += is_mid(j) && choose && key[i] == T;
         }
     }
     n_sure = __reduce_add_sync(0xffffffffu, n_sure);
@@ -162,37 +163,35 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
         sh.ties[warp] = n_tie;
     }
     __syncthreads();
-    if (warp == 0) {
-        const int s = __reduce_add_sync(0xffffffffu, sh.takes[lane]), t = __reduce_add_sync(0xffffffffu, sh.ties[lane]);
-        if (lane == 0) {
-            sh.cta_sure = s;
-            sh.cta_ties = t;
+    // of the warps, and of the CTAs, before this one
+    int at = __reduce_add_sync(0xffffffffu, lane < warp ? sh.takes[lane] : 0);
+    int ties = __reduce_add_sync(0xffffffffu, lane < warp ? sh.ties[lane] : 0);
+    if (size > 1) {
+        if (warp == kSelWarps - 1 && lane == 0) {
+            sh.cta_sure = at + n_sure;
+            sh.cta_ties = ties + n_tie;
         }
+        cluster.sync();
+        at += __reduce_add_sync(0xffffffffu, lane < rank ? *cluster.map_shared_rank(&sh.cta_sure, lane) : 0);
+        ties += __reduce_add_sync(0xffffffffu, lane < rank ? *cluster.map_shared_rank(&sh.cta_ties, lane) : 0);
     }
-    cluster.sync();
-    // kept without a choice, and equal keys, before this warp's run: of the CTAs and of the warps before
-    int at = lane < warp ? sh.takes[lane] : 0, ties = lane < warp ? sh.ties[lane] : 0;
-    if (lane < rank) {
-        at += *cluster.map_shared_rank(&sh.cta_sure, lane);
-        ties += *cluster.map_shared_rank(&sh.cta_ties, lane);
-    }
-    at = __reduce_add_sync(0xffffffffu, at);
-    ties = __reduce_add_sync(0xffffffffu, ties);
     at += min(ties, need);
     const unsigned below = (1u << lane) - 1u;
-    for (int j0 = r0; j0 < r1; j0 += 32 * kBatch) {
-        classify(j0);
+    for (int j0 = r0; j0 < r1; j0 += kRound) {
+        if (!RESIDENT) load(j0);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const unsigned tb = __ballot_sync(0xffffffffu, tie[i]);
-            const bool take = sure[i] || (tie[i] && ties + __popc(tb & below) < need);
+        for (int i = 0; i < KEYS; ++i) {
+            const int j = j0 + 32 * i + lane;
+            const bool tie = is_mid(j) && choose && key[i] == T;
+            const unsigned tb = __ballot_sync(0xffffffffu, tie);
+            const bool take = j < r1 && (!is_mid(j) || key[i] > T || (tie && ties + __popc(tb & below) < need));
             const unsigned kb = __ballot_sync(0xffffffffu, take);
-            if (take) kept[at + __popc(kb & below)] = j0 + 32 * i + lane;
+            if (take) kept[at + __popc(kb & below)] = j;
             at += __popc(kb);
             ties += __popc(tb);
         }
     }
-    cluster.sync(); // the cluster has read this CTA's counts
+    if (size > 1) cluster.sync(); // the cluster has read this CTA's counts
 }
 
 constexpr int kMoveRows = 64, kMoveThreads = 256;
@@ -275,11 +274,15 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4EvictArgs a)
 
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelShared));
-    if (e != cudaSuccess) return e;
-    // a CTA for every 8192 tokens a cache may hold
+    // keys in registers where a cluster of up to 8 CTAs holds a full cache (16 keys to a thread, 32 above
+    // 65536 tokens); longer caches are read again for every digit
+    constexpr int kCta = kSelThreads * 16;
     int size = 1;
-    while (size < kMaxCluster && (int64_t)size * 8192 < a.L_max) size *= 2;
+    while (size < kMaxCluster && (int64_t)size * kCta < a.L_max) size *= 2;
+    const auto kernel = a.L_max <= (int64_t)size * kCta ? kv4_select_kernel<16, true>
+                        : a.L_max <= (int64_t)size * kCta * 2 ? kv4_select_kernel<32, true> : kv4_select_kernel<32, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelShared));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * size));
     cfg.blockDim = dim3(kSelThreads);
@@ -291,7 +294,7 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s)
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     trace_begin(s);
-    e = cudaLaunchKernelEx(&cfg, kv4_select_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return e;
     const dim3 grid((a.keep + kMoveRows - 1) / kMoveRows, a.H_kv, a.B);
     if (a.d_h == 128)
