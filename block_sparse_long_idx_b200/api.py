@@ -9,6 +9,8 @@ If the compiled library is missing the import fails loudly: there is no fallback
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import numpy as np
@@ -435,7 +437,7 @@ def msa_sparse_prefill_fp8(q8: E4M3Rows, k8: E4M3Rows, v8: E4M3Rows, block_idx, 
 # --------------------------------------------------------------------------- 4-bit key/value cache
 def _is(t, name, dtypes, shape, device):
     """A contiguous CUDA tensor of one of `dtypes` and of `shape` on `device`, else ValueError."""
-    if not t.is_cuda or t.device != device or t.dtype not in dtypes or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {'/'.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)} "
                          f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t
@@ -466,6 +468,7 @@ class KV4Cache:
         self.B, self.H_kv, self.L_max, self.d_h, self.device = B, H_kv, L_max, 2 * half, dev
         self._c = msa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), B, H_kv,
                                 2 * half, L_max, self.k_scale, self.v_scale)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, B: int, L_max: int, H_kv: int, d_h: int, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda"):
@@ -476,35 +479,34 @@ class KV4Cache:
         return cls(rows(d_h // 2), rows(d_h // 16), rows(d_h // 2), rows(d_h // 16), k_scale, v_scale)
 
 
-class _Call:
-    """What a call of this section runs under: its tensors' device made current, the stream (the device's
-    current one unless given), and the memory that it allocates kept from reuse until that stream is done."""
+def _on_device(call):
+    """Runs a call of this section, whose tensors live on the device of its KV4Cache argument, with that device
+    current (the library launches on the current device)."""
+    at = list(inspect.signature(call).parameters).index("cache")
 
-    def __init__(self, device, stream):
-        self.device = device
-        self.own = stream is None
-        self.stream = stream
+    @functools.wraps(call)
+    def run(*args, **kw):
+        device = (args[at] if len(args) > at else kw["cache"]).device
+        if device.index == torch.cuda.current_device():
+            return call(*args, **kw)
+        with torch.cuda.device(device):
+            return call(*args, **kw)
 
-    def __enter__(self):
-        self.guard = None
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        self.handle = _stream(self.stream)
-        return self
+    return run
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
 
-    def hold(self, *tensors):
-        if self.own:
-            return
-        s = self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.handle, self.device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+def _raw_stream(device, stream):
+    """The device's current stream, or the given one, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+
+
+def _hold(stream, *tensors):
+    """Keeps memory that a call allocated from reuse until a stream other than the allocating one is done."""
+    if stream is None:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device))
 
 
 def _tables(cache, T, starts, cu_seqlens):
@@ -525,6 +527,7 @@ def _token_stride(t, name, cache):
     return t.stride(0) if t.shape[0] > 1 else cache.H_kv * cache.d_h
 
 
+@_on_device
 def msa_kv4_append(cache: KV4Cache, k, v, starts, cu_seqlens=None, workspace=None, stream=None):
     """Quantises new rows k, v [T, H_kv, d_h] (bf16; the token stride is free) into the cache: the rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 go to the positions starts[b], starts[b] + 1, ... of sequence b;
@@ -534,14 +537,14 @@ def msa_kv4_append(cache: KV4Cache, k, v, starts, cu_seqlens=None, workspace=Non
     if v.shape[0] != T:
         raise ValueError("k and v: different numbers of rows")
     _tables(cache, T, starts, cu_seqlens)
-    with _Call(cache.device, stream) as call:
-        ws = _workspace(256, cache.device, workspace)
-        _check("msa_kv4_append", lib.msa_kv4_append(
-            ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), ks, vs, T, starts.data_ptr(), _ptr(cu_seqlens),
-            ws.data_ptr(), ws.numel(), call.handle))
-        call.hold(ws if workspace is None else None)
+    ws = _workspace(256, cache.device, workspace)
+    _check("msa_kv4_append", lib.msa_kv4_append(
+        cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, T, starts.data_ptr(), _ptr(cu_seqlens), ws.data_ptr(), ws.numel(),
+        _raw_stream(cache.device, stream)))
+    _hold(stream, ws)
 
 
+@_on_device
 def msa_kv4_read(cache: KV4Cache, starts, cu_seqlens=None, T: int | None = None, k=None, v=None, workspace=None,
                  stream=None):
     """The rows that msa_kv4_append with the same starts, cu_seqlens and T writes, as bf16 values.
@@ -551,22 +554,20 @@ def msa_kv4_read(cache: KV4Cache, starts, cu_seqlens=None, T: int | None = None,
             raise ValueError("msa_kv4_read: T (the number of rows) is needed with cu_seqlens")
         T = cache.B
     _tables(cache, T, starts, cu_seqlens)
-    made = []
-    with _Call(cache.device, stream) as call:
-        for i, (t, n) in enumerate(((k, "k"), (v, "v"))):
-            if t is None:
-                made.append(torch.empty((T, cache.H_kv, cache.d_h), dtype=torch.bfloat16, device=cache.device))
-            else:
-                _is(t, n, _BF16, (T, cache.H_kv, cache.d_h), cache.device)
-        if k is None:
-            k = made[0]
-        if v is None:
-            v = made[-1]
-        ws = _workspace(256, cache.device, workspace)
-        _check("msa_kv4_read", lib.msa_kv4_read(
-            ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), T, starts.data_ptr(), _ptr(cu_seqlens), ws.data_ptr(),
-            ws.numel(), call.handle))
-        call.hold(ws if workspace is None else None, *made)
+    shape = (T, cache.H_kv, cache.d_h)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    else:
+        _is(k, "k", _BF16, shape, cache.device)
+    if v is None:
+        v = torch.empty_like(k)
+    else:
+        _is(v, "v", _BF16, shape, cache.device)
+    ws = _workspace(256, cache.device, workspace)
+    _check("msa_kv4_read", lib.msa_kv4_read(
+        cache._ref, k.data_ptr(), v.data_ptr(), T, starts.data_ptr(), _ptr(cu_seqlens), ws.data_ptr(), ws.numel(),
+        _raw_stream(cache.device, stream)))
+    _hold(stream, ws, k, v)
     return k, v
 
 
@@ -588,6 +589,7 @@ def _decode_tensors(q, cache, lens, out, lse, weights, weights_out):
     return H_q
 
 
+@_on_device
 def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weights_out=None, decay: float = 1.0, out=None,
                    lse=None, want_lse: bool = True, workspace=None, stream=None):
     """Attention of one query token per sequence (q [B, H_q, d_h]) over the first lens[b] rows of the 4-bit
@@ -601,20 +603,19 @@ def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weigh
             raise ValueError("block_idx: expected [B, H_kv, k]")
         k = block_idx.shape[2]
         _is(block_idx, "block_idx", _I32, (cache.B, cache.H_kv, k), cache.device)
-    with _Call(cache.device, stream) as call:
-        made = []
-        if out is None:
-            made.append(out := torch.empty_like(q))
-        if lse is None and want_lse:
-            made.append(lse := torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device))
-        ws = _workspace(lib.msa_kv4_decode_workspace_size(cache.B, H_q), cache.device, workspace)
-        _check("msa_kv4_decode", lib.msa_kv4_decode(
-            ctypes.byref(cache._c), q.data_ptr(), lens.data_ptr(), H_q, _ptr(block_idx), k, _ptr(weights),
-            _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), call.handle))
-        call.hold(ws if workspace is None else None, *made)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device)
+    ws = _workspace(lib.msa_kv4_decode_workspace_size(cache.B, H_q), cache.device, workspace)
+    _check("msa_kv4_decode", lib.msa_kv4_decode(
+        cache._ref, q.data_ptr(), lens.data_ptr(), H_q, _ptr(block_idx), k, _ptr(weights), _ptr(weights_out), decay,
+        out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _raw_stream(cache.device, stream)))
+    _hold(stream, ws, out, lse)
     return out, lse
 
 
+@_on_device
 def msa_sparse_decode_kv4(q, q_idx, cache: KV4Cache, k_idx_cache, lens, B_k: int = 128, k: int = 16, weights=None,
                           weights_out=None, decay: float = 1.0, out=None, lse=None, want_lse: bool = True,
                           block_idx_out=None, workspace=None, stream=None):
@@ -628,24 +629,23 @@ def msa_sparse_decode_kv4(q, q_idx, cache: KV4Cache, k_idx_cache, lens, B_k: int
     _is(k_idx_cache, "k_idx_cache", _BF16, (cache.B, cache.L_max, cache.H_kv, d_idx), cache.device)
     if block_idx_out is not None:
         _is(block_idx_out, "block_idx_out", _I32, (cache.B, cache.H_kv, k), cache.device)
-    with _Call(cache.device, stream) as call:
-        made = []
-        if out is None:
-            made.append(out := torch.empty_like(q))
-        if lse is None and want_lse:
-            made.append(lse := torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device))
-        if block_idx_out is None:
-            made.append(block_idx_out := torch.empty((cache.B, cache.H_kv, max(k, 0)), dtype=torch.int32, device=cache.device))
-        ws = _workspace(lib.msa_sparse_decode_kv4_workspace_size(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k),
-                        cache.device, workspace)
-        _check("msa_sparse_decode_kv4", lib.msa_sparse_decode_kv4(
-            ctypes.byref(cache._c), q.data_ptr(), q_idx.data_ptr(), k_idx_cache.data_ptr(), lens.data_ptr(), H_q, d_idx, B_k,
-            k, _ptr(weights), _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), block_idx_out.data_ptr(),
-            ws.data_ptr(), ws.numel(), call.handle))
-        call.hold(ws if workspace is None else None, *made)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device)
+    if block_idx_out is None:
+        block_idx_out = torch.empty((cache.B, cache.H_kv, max(k, 0)), dtype=torch.int32, device=cache.device)
+    ws = _workspace(lib.msa_sparse_decode_kv4_workspace_size(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k), cache.device,
+                    workspace)
+    _check("msa_sparse_decode_kv4", lib.msa_sparse_decode_kv4(
+        cache._ref, q.data_ptr(), q_idx.data_ptr(), k_idx_cache.data_ptr(), lens.data_ptr(), H_q, d_idx, B_k, k,
+        _ptr(weights), _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), block_idx_out.data_ptr(), ws.data_ptr(),
+        ws.numel(), _raw_stream(cache.device, stream)))
+    _hold(stream, ws, out, lse, block_idx_out)
     return out, lse, block_idx_out
 
 
+@_on_device
 def msa_kv4_evict(cache: KV4Cache, to: KV4Cache, weights, lens, keep: int, recent: int = 0, first: int = 0,
                   weights_dst=None, k_idx_cache=None, k_idx_dst=None, lens_out=None, kept=None, workspace=None,
                   stream=None):
@@ -672,16 +672,13 @@ def msa_kv4_evict(cache: KV4Cache, to: KV4Cache, weights, lens, keep: int, recen
         _is(lens_out, "lens_out", _I32, (cache.B,), dev)
     if kept is not None:
         _is(kept, "kept", _I32, (cache.B, cache.H_kv, keep), dev)
-    with _Call(dev, stream) as call:
-        made = []
-        if lens_out is None:
-            made.append(lens_out := torch.empty_like(lens))
-        if kept is None:
-            made.append(kept := torch.empty((cache.B, cache.H_kv, max(keep, 0)), dtype=torch.int32, device=dev))
-        ws = _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
-        _check("msa_kv4_evict", lib.msa_kv4_evict(
-            ctypes.byref(cache._c), ctypes.byref(to._c), weights.data_ptr(), lens.data_ptr(), keep, recent, first,
-            _ptr(k_idx_cache), _ptr(k_idx_dst), d_idx, _ptr(weights_dst), lens_out.data_ptr(), kept.data_ptr(),
-            ws.data_ptr(), ws.numel(), call.handle))
-        call.hold(ws if workspace is None else None, *made)
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if kept is None:
+        kept = torch.empty((cache.B, cache.H_kv, max(keep, 0)), dtype=torch.int32, device=dev)
+    ws = _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
+    _check("msa_kv4_evict", lib.msa_kv4_evict(
+        cache._ref, to._ref, weights.data_ptr(), lens.data_ptr(), keep, recent, first, _ptr(k_idx_cache), _ptr(k_idx_dst),
+        d_idx, _ptr(weights_dst), lens_out.data_ptr(), kept.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev, stream)))
+    _hold(stream, ws, lens_out, kept)
     return lens_out, kept

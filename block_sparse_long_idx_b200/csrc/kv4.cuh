@@ -8,6 +8,8 @@
 // Head-major: codes [B][H_kv][L_max][d_h / 2], scales [B][H_kv][L_max][d_h / 16], so that the tokens
 // of a (sequence, head) are one contiguous run a bulk copy can stream.
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -71,6 +73,25 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
 }
+
+// Raises a kernel's dynamic shared memory limit, once per device (the call costs as much as a launch).
+class SmemOptIn {
+    std::atomic<uint64_t> done_{0}; // one bit per device; devices from 64 on are set every time
+
+public:
+    template <class F>
+    cudaError_t set(F* kernel, int bytes)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+        if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // Rows of a packed batch: row i of T belongs to the sequence b with cu[b] <= i < cu[b + 1] (cu =
 // nullptr: one row per sequence) and to position starts[b] + i - cu[b] of its cache.

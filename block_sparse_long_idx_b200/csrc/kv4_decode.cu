@@ -779,8 +779,8 @@ __global__ void __launch_bounds__(256) kv4_decay_kernel(Kv4DecodeArgs a)
 template <int DH, bool GIVEN>
 cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<DH, GIVEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DH>::SMEM);
-    if (e != cudaSuccess) return e;
+    static SmemOptIn opt_in;
+    if (cudaError_t e = opt_in.set(kv4_decode_kernel<DH, GIVEN>, Cfg<DH>::SMEM)) return e;
     trace_begin(s);
     kv4_decode_kernel<DH, GIVEN><<<kKv4Ctas, kLaunch, Cfg<DH>::SMEM, s>>>(a);
     trace_end(s, MSA_KERNEL_KV4_ATTN);

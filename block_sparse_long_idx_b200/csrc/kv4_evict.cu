@@ -36,8 +36,9 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 }
 
 struct SelShared {
-    int hist[kDigits][kBins * kCopies];
-    int sums[2][kBins]; // of the CTA's copies, read by the cluster: digits alternate, so one barrier each is enough
+    // digits alternate between two histograms, so that one barrier each is enough (and two CTAs fit an SM)
+    int hist[2][kBins * kCopies];
+    int sums[2][kBins]; // of the CTA's copies, read by the cluster
     int tmp[kSelWarps];
     uint32_t prefix; // of the key looked for, and how many of its equals are still to be taken
     int need;
@@ -87,24 +88,28 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
     int need = a.keep - a.first - a.recent;
     const bool choose = need > 0;
     if (choose) {
-        for (int i = tid; i < kDigits * kBins * kCopies / 4; i += kSelThreads)
-            reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
+        auto clear = [&](int* h) {
+            for (int i = tid; i < kBins * kCopies / 4; i += kSelThreads) reinterpret_cast<int4*>(h)[i] = make_int4(0, 0, 0, 0);
+        };
+        clear(sh.hist[0]);
+        clear(sh.hist[1]);
         __syncthreads();
         T = 0;
         for (int d = 0; d < kDigits; ++d) {
             const int shift = digit_shift(d), bits = digit_bits(d);
             const uint32_t above = d == 0 ? 0u : 0xFFFFFFFFu << (shift + bits);
+            if (d == 1) clear(sh.hist[0]); // for the last digit: every thread has read the first one's
             for (int j0 = r0; j0 < r1; j0 += kRound) {
                 if (!RESIDENT) load(j0);
 #pragma unroll
                 for (int i = 0; i < KEYS; ++i)
                     if (is_mid(j0 + 32 * i + lane) && (key[i] & above) == T)
-                        atomicAdd(&sh.hist[d][((key[i] >> shift) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
+                        atomicAdd(&sh.hist[d & 1][((key[i] >> shift) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
             }
             __syncthreads();
             int* sums = sh.sums[d & 1];
             for (int i = tid; i < kBins; i += kSelThreads) {
-                const int4 h = *reinterpret_cast<const int4*>(&sh.hist[d][i * kCopies]);
+                const int4 h = *reinterpret_cast<const int4*>(&sh.hist[d & 1][i * kCopies]);
                 sums[i] = h.x + h.y + h.z + h.w;
             }
             cluster.sync();
@@ -279,9 +284,10 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s)
     constexpr int kCta = kSelThreads * 16;
     int size = 1;
     while (size < kMaxCluster && (int64_t)size * kCta < a.L_max) size *= 2;
-    const auto kernel = a.L_max <= (int64_t)size * kCta ? kv4_select_kernel<16, true>
-                        : a.L_max <= (int64_t)size * kCta * 2 ? kv4_select_kernel<32, true> : kv4_select_kernel<32, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelShared));
+    const int which = a.L_max <= (int64_t)size * kCta ? 0 : (a.L_max <= (int64_t)size * kCta * 2 ? 1 : 2);
+    const auto kernel = which == 0 ? kv4_select_kernel<16, true> : (which == 1 ? kv4_select_kernel<32, true> : kv4_select_kernel<32, false>);
+    static SmemOptIn opt_in[3];
+    cudaError_t e = opt_in[which].set(kernel, (int)sizeof(SelShared));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * size));
