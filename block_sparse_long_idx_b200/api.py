@@ -531,17 +531,17 @@ def _token_stride(t, name, cache):
 def msa_kv4_append(cache: KV4Cache, k, v, starts, cu_seqlens=None, workspace=None, stream=None):
     """Quantises new rows k, v [T, H_kv, d_h] (bf16; the token stride is free) into the cache: the rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 go to the positions starts[b], starts[b] + 1, ... of sequence b;
-    without cu_seqlens T = B, one row per sequence. starts, cu_seqlens: int32 device tensors."""
+    without cu_seqlens T = B, one row per sequence. starts, cu_seqlens: int32 device tensors. Rows outside the
+    cache are left out; a workspace (optional, msa_kv4_rows_workspace_size bytes) tells msa_get_device_error."""
     T = k.shape[0]
     ks, vs = _token_stride(k, "k", cache), _token_stride(v, "v", cache)
     if v.shape[0] != T:
         raise ValueError("k and v: different numbers of rows")
     _tables(cache, T, starts, cu_seqlens)
-    ws = _workspace(256, cache.device, workspace)
+    ws = None if workspace is None else _workspace(lib.msa_kv4_rows_workspace_size(), cache.device, workspace)
     _check("msa_kv4_append", lib.msa_kv4_append(
-        cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, T, starts.data_ptr(), _ptr(cu_seqlens), ws.data_ptr(), ws.numel(),
+        cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, T, starts.data_ptr(), _ptr(cu_seqlens), _ptr(ws), 0 if ws is None else ws.numel(),
         _raw_stream(cache.device, stream)))
-    _hold(stream, ws)
 
 
 @_on_device
@@ -563,11 +563,11 @@ def msa_kv4_read(cache: KV4Cache, starts, cu_seqlens=None, T: int | None = None,
         v = torch.empty_like(k)
     else:
         _is(v, "v", _BF16, shape, cache.device)
-    ws = _workspace(256, cache.device, workspace)
+    ws = None if workspace is None else _workspace(lib.msa_kv4_rows_workspace_size(), cache.device, workspace)
     _check("msa_kv4_read", lib.msa_kv4_read(
-        cache._ref, k.data_ptr(), v.data_ptr(), T, starts.data_ptr(), _ptr(cu_seqlens), ws.data_ptr(), ws.numel(),
+        cache._ref, k.data_ptr(), v.data_ptr(), T, starts.data_ptr(), _ptr(cu_seqlens), _ptr(ws), 0 if ws is None else ws.numel(),
         _raw_stream(cache.device, stream)))
-    _hold(stream, ws, k, v)
+    _hold(stream, k, v)
     return k, v
 
 
@@ -589,6 +589,11 @@ def _decode_tensors(q, cache, lens, out, lse, weights, weights_out):
     return H_q
 
 
+@functools.lru_cache
+def _kv4_decode_bytes(B, H_q):
+    return lib.msa_kv4_decode_workspace_size(B, H_q)
+
+
 @_on_device
 def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weights_out=None, decay: float = 1.0, out=None,
                    lse=None, want_lse: bool = True, workspace=None, stream=None):
@@ -607,7 +612,7 @@ def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weigh
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device)
-    ws = _workspace(lib.msa_kv4_decode_workspace_size(cache.B, H_q), cache.device, workspace)
+    ws = _workspace(_kv4_decode_bytes(cache.B, H_q), cache.device, workspace)
     _check("msa_kv4_decode", lib.msa_kv4_decode(
         cache._ref, q.data_ptr(), lens.data_ptr(), H_q, _ptr(block_idx), k, _ptr(weights), _ptr(weights_out), decay,
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _raw_stream(cache.device, stream)))
@@ -676,9 +681,10 @@ def msa_kv4_evict(cache: KV4Cache, to: KV4Cache, weights, lens, keep: int, recen
         lens_out = torch.empty_like(lens)
     if kept is None:
         kept = torch.empty((cache.B, cache.H_kv, max(keep, 0)), dtype=torch.int32, device=dev)
-    ws = _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
+    ws = None if workspace is None else _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
     _check("msa_kv4_evict", lib.msa_kv4_evict(
         cache._ref, to._ref, weights.data_ptr(), lens.data_ptr(), keep, recent, first, _ptr(k_idx_cache), _ptr(k_idx_dst),
-        d_idx, _ptr(weights_dst), lens_out.data_ptr(), kept.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev, stream)))
-    _hold(stream, ws, lens_out, kept)
+        d_idx, _ptr(weights_dst), lens_out.data_ptr(), kept.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+        _raw_stream(dev, stream)))
+    _hold(stream, lens_out, kept)
     return lens_out, kept

@@ -34,13 +34,13 @@ __device__ __forceinline__ int64_t locate_row(const Kv4RowsArgs& a, int64_t i)
         b = lo;
         off = i - a.cu[b];
         if (off < 0 || i >= a.cu[b + 1]) {
-            report_error(a.err, MSA_ERR_DEVICE_CHECK, 300);
+            if (a.err) report_error(a.err, MSA_ERR_DEVICE_CHECK, 300);
             return -1;
         }
     }
     const int start = a.starts[b];
     if (start < 0 || start + off >= a.L_max) {
-        report_error(a.err, MSA_ERR_DEVICE_CHECK, 301);
+        if (a.err) report_error(a.err, MSA_ERR_DEVICE_CHECK, 301);
         return -1;
     }
     return (int64_t)b * a.H_kv * a.L_max + start + off;

@@ -107,7 +107,7 @@ struct Kv4RowsArgs {
     const int32_t* cu;
     int64_t T, L_max;
     int B, H_kv, d_h;
-    int* err;
+    int* err; // nullptr: nothing is reported
 };
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s);
@@ -149,7 +149,7 @@ struct Kv4EvictArgs {
     int32_t* kept; // [B][H_kv][keep]
     int B, H_kv, d_h, d_idx, keep, recent, first;
     int64_t L_max, L_to;
-    int* err;
+    int* err; // nullptr: nothing is reported
 };
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s);
 

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
     const int n = bad ? 0 : len, left = min(n, a.keep);
     int32_t* kept = a.kept + (int64_t)seg * a.keep;
     if (tid == 0 && rank == 0 && seg % a.H_kv == 0) {
-        if (bad) report_error(a.err, MSA_ERR_DEVICE_CHECK, 200 + b);
+        if (bad && a.err) report_error(a.err, MSA_ERR_DEVICE_CHECK, 200 + b);
         a.lens_to[b] = left;
     }
     if (n <= a.keep) { // the whole cluster

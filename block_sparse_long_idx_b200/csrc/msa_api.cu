@@ -1069,14 +1069,20 @@ static Kv4RowsArgs kv4_rows_args(const msa_kv4_cache* c, int64_t T, const int32_
 static msa_status kv4_rows_check(const msa_kv4_cache* c, const void* k, const void* v, int64_t T, const int32_t* starts,
                                  const int32_t* cu, const void* workspace, size_t workspace_bytes)
 {
-    if (T < 0 || (T > 0 && (!k || !v)) || !starts || !workspace) return MSA_ERR_INVALID_ARG;
+    if (T < 0 || (T > 0 && (!k || !v)) || !starts) return MSA_ERR_INVALID_ARG;
     if (msa_status st = kv4_check(c)) return st;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(cu, 4) || !aligned(workspace, 256) ||
         (!cu && T != c->B))
         return MSA_ERR_INVALID_ARG;
     if (T > kv4_rows(c)) return MSA_ERR_INVALID_ARG; // more rows than the cache has
-    if (workspace_bytes < kErrBytes) return MSA_ERR_WORKSPACE;
+    if (workspace && workspace_bytes < kErrBytes) return MSA_ERR_WORKSPACE;
     return MSA_OK;
+}
+
+// The error word of calls whose workspace is optional: cleared where there is one.
+static msa_status kv4_clear_error(void* workspace, cudaStream_t s)
+{
+    return workspace ? cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word") : MSA_OK;
 }
 
 msa_status msa_kv4_append(const msa_kv4_cache* cache, const msa_bf16* k, const msa_bf16* v, int64_t k_stride,
@@ -1088,7 +1094,7 @@ msa_status msa_kv4_append(const msa_kv4_cache* cache, const msa_bf16* k, const m
     if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0) return MSA_ERR_INVALID_ARG;
     if (injected("msa_kv4_append")) return MSA_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
+    if (msa_status st0 = kv4_clear_error(workspace, s)) return st0;
     if (T == 0) return MSA_OK;
     Kv4RowsArgs a = kv4_rows_args(cache, T, starts, cu_seqlens, workspace);
     a.x[0] = k;
@@ -1107,7 +1113,7 @@ msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf16* v, in
     if (msa_status st = kv4_rows_check(cache, k, v, T, starts, cu_seqlens, workspace, workspace_bytes)) return st;
     if (injected("msa_kv4_read")) return MSA_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
+    if (msa_status st0 = kv4_clear_error(workspace, s)) return st0;
     if (T == 0) return MSA_OK;
     Kv4RowsArgs a = kv4_rows_args(cache, T, starts, cu_seqlens, workspace);
     a.y[0] = k;
@@ -1251,7 +1257,7 @@ msa_status msa_kv4_evict(const msa_kv4_cache* cache, const msa_kv4_cache* to, co
                          int recent, int first, const msa_bf16* k_idx, msa_bf16* k_idx_to, int d_idx, float* w_to,
                          int32_t* lens_to, int32_t* kept, void* workspace, size_t workspace_bytes, msa_stream_t stream)
 {
-    if (!w || !lens || !lens_to || !kept || !workspace || keep < 1 || recent < 0 || first < 0 ||
+    if (!w || !lens || !lens_to || !kept || keep < 1 || recent < 0 || first < 0 ||
         (int64_t)recent + first > keep || !k_idx != !k_idx_to || (k_idx && d_idx < 1))
         return MSA_ERR_INVALID_ARG;
     if (msa_status st = kv4_check(cache)) return st;
@@ -1274,10 +1280,10 @@ msa_status msa_kv4_evict(const msa_kv4_cache* cache, const msa_kv4_cache* to, co
     for (const auto& x : src)
         for (const auto& y : dst)
             if (overlap(x.p, x.bytes, y.p, y.bytes)) return MSA_ERR_INVALID_ARG;
-    if (workspace_bytes < msa_kv4_evict_workspace_size(B, H_kv, keep)) return MSA_ERR_WORKSPACE;
+    if (workspace && workspace_bytes < msa_kv4_evict_workspace_size(B, H_kv, keep)) return MSA_ERR_WORKSPACE;
     if (injected("msa_kv4_evict")) return MSA_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
+    if (msa_status st0 = kv4_clear_error(workspace, s)) return st0;
     Kv4EvictArgs a{};
     a.k_codes = cache->k_codes;
     a.k_scales = cache->k_scales;

@@ -386,8 +386,10 @@ MSA_API msa_status msa_sparse_decode(const msa_bf16* q, const msa_bf16* q_idx, c
  * H_q / H_kv any whole number up to 16, B * H_kv up to 65535, t positive and finite.
  *
  * Every call takes a workspace of at least the size its query returns (256-byte aligned; the device
- * error word is at its start). Two calls that overlap in time need workspaces of their own. Captured
- * calls may be replayed; the calls' device tensors (lens, starts, cu_seqlens) are read on replay.
+ * error word is at its start). msa_kv4_append, msa_kv4_read and msa_kv4_evict use it for the error word
+ * alone and take NULL too: what they would report is then left out without a report. Two calls that
+ * overlap in time need workspaces of their own. Captured calls may be replayed; the calls' device
+ * tensors (lens, starts, cu_seqlens) are read on replay.
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
     uint8_t *k_codes, *k_scales, *v_codes, *v_scales; /* device */

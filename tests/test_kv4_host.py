@@ -77,7 +77,7 @@ def test_rows_validation(msa):
     assert app(ks=255) == INVALID and app(ks=248) == INVALID and app(vs=260) == INVALID   # below a row; not a multiple of 8
     assert app(T=-1) == INVALID and app(cu=None) == INVALID                                # T rows need T = B without tables
     assert app(T=4 * 2 * 1024 + 1) == INVALID                                              # more rows than the cache has
-    assert app(cu=P2 + 2) == INVALID and app(ws=None) == INVALID and app(ws=WS + 16) == INVALID
+    assert app(cu=P2 + 2) == INVALID and app(ws=WS + 16) == INVALID
     assert app(n=need - 1) == WORKSPACE
     rd = caller(msa.lib.msa_kv4_read, ["cache", "k", "v", "T", "starts", "cu", "ws", "n", "stream"],
                 [cache(msa), P2, P2, 9, P2, P2, WS, need, None])
