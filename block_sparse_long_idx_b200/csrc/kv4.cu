@@ -53,13 +53,13 @@ __device__ __forceinline__ void locate_rows(const Kv4RowsArgs& a, int64_t i0, in
     __syncthreads();
 }
 
-// Correctly rounded x / d, two at a time, from r = 1 / d correctly rounded (Markstein's correction of x * r
-// by its exact residual), for d > 0 and where nothing over- or underflows: see quantise16. A zero may lose
-// its sign.
-__device__ __forceinline__ uint64_t quotient2(uint64_t x, float d, float r)
+// Correctly rounded -x / d, two at a time, from nr = -1 / d correctly rounded (Markstein's correction of the
+// product by its exact residual), for d > 0 and where nothing over- or underflows: see quantise16. The
+// residual is taken as q d + x, so that a zero keeps its sign.
+__device__ __forceinline__ uint64_t minus_quotient2(uint64_t x, uint64_t d, uint64_t nr)
 {
-    const uint64_t rr = f2_pack(r, r), q = f2_mul(x, rr), nq = q ^ 0x8000000080000000ull;
-    return f2_fma(f2_fma(nq, f2_pack(d, d), x), rr, q);
+    const uint64_t q = f2_mul(x, nr);
+    return f2_fma(f2_fma(q, d, x), nr, q);
 }
 
 // The 16 elements of w as codes c and their scale's byte. rt = 1 / t, or 0 where t is outside [2^-20,
@@ -74,28 +74,34 @@ __device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], float t, 
     m = max(m >> 16, m & 0xFFFFu);
     float amax = __uint_as_float(m << 16);
     c[0] = c[1] = 0u;
-    if (rt == 0.f || !(amax < 0x1p100f)) {
-        amax = __fdiv_rn(amax, t); // rounding keeps the order
-        const uint32_t s8 = e4m3x2_pack(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu;
-        if (s8 == 0) return 0u;
-        const float s = e4m3x2_unpack(s8).x;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            c[e >> 2] |= e2m1x2_pack(__fdiv_rn(__fdiv_rn(bf16_lo(w[e]), t), s), __fdiv_rn(__fdiv_rn(bf16_hi(w[e]), t), s)) << (8 * (e & 3));
-        return s8;
-    }
-    if (t != 1.f) amax = f2_lo(quotient2(f2_pack(amax, 0.f), t, rt));
+    const bool plain = rt == 0.f || !(amax < 0x1p100f);
+    if (t != 1.f) amax = __fdiv_rn(amax, t); // rounding keeps the order
     const uint32_t s8 = e4m3x2_pack(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu;
     if (s8 == 0) return 0u;
-    const float s = e4m3x2_unpack(s8).x, rs = __frcp_rn(s);
+    const float s = e4m3x2_unpack(s8).x;
+    float q[16];
+    if (plain) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float lo = bf16_lo(w[e]), hi = bf16_hi(w[e]);
-        uint64_t y = f2_pack(lo, hi);
-        if (t != 1.f) y = quotient2(y, t, rt);
-        const uint64_t q = quotient2(y, s, rs);
-        c[e >> 2] |= e2m1x2_pack(copysignf(f2_lo(q), lo), copysignf(f2_hi(q), hi)) << (8 * (e & 3));
+        for (int e = 0; e < 8; ++e) {
+            q[2 * e] = __fdiv_rn(__fdiv_rn(bf16_lo(w[e]), t), s);
+            q[2 * e + 1] = __fdiv_rn(__fdiv_rn(bf16_hi(w[e]), t), s);
+        }
+    } else {
+        const float rs = __frcp_rn(s);
+        const uint64_t ss = f2_pack(s, s), nrs = f2_pack(-rs, -rs), tt = f2_pack(t, t), nrt = f2_pack(-rt, -rt);
+        const uint32_t flip = t != 1.f ? 0u : 0x80008000u; // either way y below is -x / t
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t v = w[e] ^ flip;
+            uint64_t y = f2_pack(bf16_lo(v), bf16_hi(v));
+            if (t != 1.f) y = minus_quotient2(y, tt, nrt);
+            y = minus_quotient2(y, ss, nrs);
+            q[2 * e] = f2_lo(y);
+            q[2 * e + 1] = f2_hi(y);
+        }
     }
+    c[0] = e2m1x8_pack(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
+    c[1] = e2m1x8_pack(q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]);
     return s8;
 }
 

@@ -25,15 +25,18 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4])
         : "r"(w));
 }
 
-// Two fp32 values -> one byte of two E2M1 codes (lo in the low nibble), nearest, ties to the even
-// code, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1x2_pack(float lo, float hi)
+// Eight fp32 values -> eight E2M1 codes, the first in the lowest nibble: nearest, ties to the even code,
+// saturating at 6.
+__device__ __forceinline__ uint32_t e2m1x8_pack(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7)
 {
     uint32_t r;
-    asm("{\n\t.reg .b8 b, z;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, z, z, z};\n\t}"
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(lo), "f"(hi));
-    return r & 0xFFu;
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
+    return r;
 }
 
 // Two E4M3 bytes (bits 0-7 and 8-15 of v) -> an fp16 pair (exact).

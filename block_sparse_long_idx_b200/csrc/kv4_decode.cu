@@ -683,8 +683,9 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
     }
 }
 
-// Accumulated weights, after the attention (they need the final lse): K is read once more, and every
-// visible key of the list gets its group's sum of softmax weights. A warp takes 32 keys at a time.
+// Accumulated weights, after the attention (they need the final lse): K is read once more. A warp takes 32
+// visible keys at a time and writes decay * w_in plus the group's sum of softmax weights; with given blocks
+// the keys of the others get decay * w_in alone.
 constexpr int kWThreads = 256;
 
 template <int DH, bool GIVEN>
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
     __shared__ int warp_units[kWThreads / 32], b0, seg0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.H_q / a.H_kv;
-    const Work<GIVEN> w{a};
+    const Work<false> w{a}; // all visible blocks
     int before, b_lo, b_hi;
     const int total = total_units<kWThreads>(w, warp_units, before, b_lo, b_hi);
     const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
@@ -708,72 +709,69 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         before += n;
     }
     __syncthreads();
-    Walk<GIVEN> cons;
+    const bool rest = !(a.w_in == a.w_out && a.decay == 1.f); // keys of other blocks change too
+    Walk<false> cons;
     for (cons.begin(w, b0, seg0, lo, hi); cons.more(); cons.next_segment(w)) {
         if (cons.pos >= cons.end) continue;
         uint32_t qf[DH / 16][4];
         float f0, f1;
         load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
+        auto qget = [&](int i, uint32_t (&v)[4]) { v[0] = qf[i][0], v[1] = qf[i][1], v[2] = qf[i][2], v[3] = qf[i][3]; };
         const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
         const float z0 = g < G ? lse[g] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
         const float z1 = g + 8 < G ? lse[g + 8] * 1.4426950408889634f : CUDART_INF_F;
-        auto qget = [&](int i, uint32_t (&v)[4]) { v[0] = qf[i][0], v[1] = qf[i][1], v[2] = qf[i][2], v[3] = qf[i][3]; };
+        int mine = -1; // given blocks: the first key of this lane's
+        if (GIVEN && lane < a.k) mine = Work<true>{a}.key0(cons.b, cons.r, lane, cons.len);
         const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
         const int my_key = 8 * (g >> 1) + t + 4 * (g & 1);
-        // the next tile of this warp with visible keys: its rows and the lane's old weight are loaded one tile ahead
+        // the next tile of this warp that has work: its rows and the lane's old weight are loaded one tile ahead
         int next = 4 * cons.pos + warp;
         struct Ahead {
             KTile<DH> k;
             int64_t row; // first row, -1: none
             int nk;
+            bool chosen;
             float old;
         } ahead;
         auto fetch = [&] {
             ahead.row = -1;
             for (; next < 4 * cons.end && ahead.row < 0; next += kWThreads / 32) {
-                const int blk = w.key0(cons.b, cons.r, next / 4 - cons.seg, cons.len), key0 = blk + kTile * (next & 3);
+                const int key0 = (next - 4 * cons.seg) * kTile;
                 ahead.nk = min(kTile, cons.len - key0);
-                if (blk < 0 || ahead.nk <= 0) continue;
+                ahead.chosen = !GIVEN || __any_sync(0xffffffffu, mine == key0 / kBk * kBk);
+                if (ahead.nk <= 0 || !(ahead.chosen || rest)) continue;
                 ahead.row = row0 + key0;
-                ahead.k.load(a.k_codes + ahead.row * C::CODE, a.k_scales + ahead.row * C::NG, g, t);
-                // given blocks: kv4_decay_kernel has written decay * w_in to every visible key
-                ahead.old = my_key >= ahead.nk ? 0.f : (GIVEN ? a.w_out[ahead.row + my_key] : (a.w_in ? a.decay * a.w_in[ahead.row + my_key] : 0.f));
+                if (ahead.chosen) ahead.k.load(a.k_codes + ahead.row * C::CODE, a.k_scales + ahead.row * C::NG, g, t);
+                ahead.old = my_key < ahead.nk && a.w_in ? a.decay * a.w_in[ahead.row + my_key] : 0.f;
             }
         };
         fetch();
         while (ahead.row >= 0) {
             const Ahead now = ahead;
             fetch();
-            float x[4][4];
-            scores<DH>(now.k, qget, x);
-            // the heads' weights of key v = 2 n + e (the lane's columns): summed over the lanes g, which end with key g
-            float p[8];
+            float add = 0.f;
+            if (now.chosen) {
+                float x[4][4];
+                scores<DH>(now.k, qget, x);
+                // the heads' weights of key v = 2 n + e (the lane's columns): summed over the lanes g, which end with key g
+                float p[8];
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-                p[v] = ex2_approx(fmaf(x[v >> 1][v & 1], f0, -z0)) + ex2_approx(fmaf(x[v >> 1][2 + (v & 1)], f1, -z1));
+                for (int v = 0; v < 8; ++v)
+                    p[v] = ex2_approx(fmaf(x[v >> 1][v & 1], f0, -z0)) + ex2_approx(fmaf(x[v >> 1][2 + (v & 1)], f1, -z1));
 #pragma unroll
-            for (int half = 4; half > 0; half >>= 1) {
-                const bool up = g & half;
+                for (int half = 4; half > 0; half >>= 1) {
+                    const bool up = g & half;
 #pragma unroll
-                for (int v = 0; v < half; ++v) {
-                    const float give = up ? p[v] : p[v + half], keep = up ? p[v + half] : p[v];
-                    p[v] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+                    for (int v = 0; v < half; ++v) {
+                        const float give = up ? p[v] : p[v + half], keep = up ? p[v + half] : p[v];
+                        p[v] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+                    }
                 }
+                add = p[0];
             }
-            if (my_key < now.nk) a.w_out[now.row + my_key] = now.old + p[0];
+            if (my_key < now.nk) a.w_out[now.row + my_key] = now.old + add;
         }
     }
-}
-
-// w_out = decay * w_in (0 without w_in) on the visible keys of every valid sequence.
-__global__ void __launch_bounds__(256) kv4_decay_kernel(Kv4DecodeArgs a)
-{
-    const int b = blockIdx.y / a.H_kv;
-    const int len = a.lens[b];
-    if (len < a.min_len || len > a.L_max) return;
-    const int64_t base = (int64_t)blockIdx.y * a.L_max;
-    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < len; j += (int64_t)gridDim.x * 256)
-        a.w_out[base + j] = a.w_in ? a.decay * a.w_in[base + j] : 0.f;
 }
 
 template <int DH, bool GIVEN>
@@ -787,10 +785,6 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
     note_launch(1);
     if (!a.w_out) return cudaGetLastError();
     trace_begin(s);
-    if (GIVEN && !(a.w_in == a.w_out && a.decay == 1.f)) {
-        kv4_decay_kernel<<<dim3(8, a.B * a.H_kv), 256, 0, s>>>(a);
-        note_launch(1);
-    }
     kv4_weights_kernel<DH, GIVEN><<<2 * kKv4Ctas, kWThreads, 0, s>>>(a);
     note_launch(1);
     trace_end(s, MSA_KERNEL_KV4_WEIGHTS);
