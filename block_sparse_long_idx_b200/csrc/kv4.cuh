@@ -96,6 +96,24 @@ public:
     }
 };
 
+// Launch whose CTAs may start before the stream's previous kernel has ended (they call pdl_wait() before
+// they read what it wrote; every CTA calls it, so that the launch ends after that kernel).
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Rows of a packed batch: row i of T belongs to the sequence b with cu[b] <= i < cu[b + 1] (cu =
 // nullptr: one row per sequence) and to position starts[b] + i - cu[b] of its cache.
 struct Kv4RowsArgs {
@@ -129,10 +147,10 @@ struct Kv4DecodeArgs {
     int B, H_q, H_kv, d_h, k;
     int64_t L_max;
     int min_len;          // smallest valid length: 0, or 1 for the block-sparse decode
+    bool after_topk;      // the blocks are those of the Top-k kernel just launched, which has cleared the error word
     uint16_t* out;        // [B][H_q][d_h]
     float* lse;           // [B][H_q], or nullptr
     float* parts;         // [2 * kKv4Ctas][kKv4PartFloats]
-    int* arrived;         // [kKv4Ctas], zero at launch
     const float* w_in;    // [B][H_kv][L_max], or nullptr
     float* w_out;         // [B][H_kv][L_max], or nullptr: no weights (lse is set when it is not)
     float decay;

@@ -9,8 +9,7 @@
 // ragged batches and single long sequences load every SM alike. Bulk copies bring kBlocks blocks at a
 // time into a ring of kStages such chunks; every warp takes 32 keys of a chunk and keeps a running
 // maximum, sum and output of its own, joined when the CTA leaves a (sequence, KV head). What several
-// CTAs hold of one pair is joined by the CTA that finishes last, in a fixed order (results do not
-// depend on timing).
+// CTAs hold of one pair is joined by a second kernel, in a fixed order (results do not depend on timing).
 //
 // The heads of a KV head are the 16 rows of mma.sync m16n8k16 (a 16-row problem is below the 128-row
 // tcgen05 tile). E2M1 codes become fp16 pairs with the hardware conversion, times the E4M3 scale
@@ -57,8 +56,6 @@ struct Cfg {
     // join scratch: [slot][16 rows][4 lanes][DH / 4], padded so that 16-byte accesses do not conflict
     static constexpr int LANE = DH / 4 + 4, ROW = 4 * LANE, WARP = 16 * ROW;
     static constexpr int SMEM = kStages * STAGE + kSlots * WARP * 4;
-    // the join of several CTAs' partials uses it for its groups of threads (at most 12): outputs, maxima and sums
-    static_assert(kThreads / 128 * 16 * DH + kThreads / 32 * 32 <= kSlots * WARP, "scratch of the partials' join");
 };
 
 // The flattened list: a segment is a (sequence, KV head); sequence b owns H_kv segments of kJoin units (no
@@ -168,7 +165,6 @@ struct Shared {
     uint4 q[8][32]; // Q fragments of the segment
     int warp_units[kLaunch / 32];
     int b0, seg0; // sequence holding the slice's first unit, first unit of that sequence
-    int last;     // this CTA joins the partials of the segment
     int abort_flag;
 };
 
@@ -319,7 +315,11 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
     const int n_cta = min((total + kJoin + kBlocks - 1) / (kJoin + kBlocks), (int)gridDim.x); // a chunk or more for each
     const int cta = blockIdx.x;
     // sequences without keys have no units: the last CTA answers for them, and reports what is rejected
+    pdl_trigger();
+    if (GIVEN) pdl_wait(); // for the blocks
     if (cta == (int)gridDim.x - 1) {
+        if (tid == 0 && !a.after_topk) a.err[0] = a.err[1] = 0;
+        __syncthreads();
         for (int b = warp; b < a.B; b += kLaunch / 32) {
             const int len = a.lens[b];
             if (!w.valid(len)) {
@@ -624,62 +624,73 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 }
             }
         }
-        if (!whole) {
-            // the CTAs with blocks of this segment: that of its first block .. that of its last
-            const int c0 = (int)(((int64_t)(cons.seg + 1) * n_cta - 1) / total);
-            const int c1 = (int)(((int64_t)(cons.seg + cons.n) * n_cta - 1) / total);
-            __threadfence();
-            sync_consumers();
-            if (tid == 0) sh.last = atomicAdd(&a.arrived[c0], 1) == c1 - c0;
-            sync_consumers();
-            if (sh.last) {
-                __threadfence();
-                const int np = c1 - c0 + 1;
-                const int lo0 = (int)((int64_t)total * c0 / n_cta);
-                // slot of CTA c: the segment is its slice's first unless the slice starts before it (only c0's can)
-                const float* parts = a.parts + (int64_t)2 * c0 * kKv4PartFloats;
-                const int first = cons.seg > lo0 ? 1 : 0;
-                auto slot = [&](int c) { return parts + (int64_t)(c == 0 ? first : 2 * c) * kKv4PartFloats; };
-                // groups of threads take every (number of groups)-th partial, each thread up to 4 x 4 elements, with a
-                // running maximum, so that all loads of a step are independent
-                const int n4 = G * (DH / 4), width = n4 >= 128 ? 128 : (n4 >= 64 ? 64 : 32), groups = kThreads / width;
-                const int grp = tid / width, e0 = tid % width;
-                float M[4], L[4];
-                float4 acc[4] = {};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) M[u] = -CUDART_INF_F, L[u] = 0.f;
-#pragma unroll 4
-                for (int c = grp; c < np; c += groups) {
-                    const float* p = slot(c);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int e = min(e0 + u * width, n4 - 1), row = e / (DH / 4);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
-                        const float m = __ldcg(p + 16 * 128 + row), l = __ldcg(p + 16 * 128 + 16 + row);
-                        merge(M[u], L[u], acc[u], m, l, v);
-                    }
-                }
-                float4* s4 = reinterpret_cast<float4*>(join);
-                float2* ml = reinterpret_cast<float2*>(s4 + groups * n4);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int e = e0 + u * width;
-                    if (e < n4) {
-                        s4[grp * n4 + e] = acc[u];
-                        if (e % (DH / 4) == 0) ml[grp * 16 + e / (DH / 4)] = make_float2(M[u], L[u]);
-                    }
-                }
-                sync_consumers();
-                for (int e = tid; e < n4; e += kThreads) {
-                    const int row = e / (DH / 4);
-                    float Mr = -CUDART_INF_F, Lr = 0.f;
-                    float4 v = {};
-                    for (int i = 0; i < groups; ++i) merge(Mr, Lr, v, ml[i * 16 + row].x, ml[i * 16 + row].y, s4[i * n4 + e]);
-                    finish(a, (int64_t)cons.b * a.H_q + cons.r * G + row, e % (DH / 4) * 4, v, Mr, Lr);
-                }
+        sync_consumers(); // the join scratch is free again
+    }
+}
+
+// Joins the partials of the segments that several CTAs share. CTA (c, y): the segment whose first block is in
+// CTA c's slice and whose last is not (there is at most one), heads kJoinRows y and on; kJoinGroups warps a
+// head, each with every kJoinGroups-th partial, in a fixed order.
+constexpr int kJoinRows = 4, kJoinGroups = 4, kJoinThreads = kJoinRows * kJoinGroups * 32;
+
+template <int DH, bool GIVEN>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeArgs a)
+{
+    constexpr int L4 = DH / 4; // lanes with 4 elements each
+    __shared__ int warp_units[kJoinThreads / 32], found[4];
+    __shared__ float4 sv[kJoinRows][kJoinGroups][L4];
+    __shared__ float2 sml[kJoinRows][kJoinGroups];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_trigger();
+    const Work<GIVEN> w{a};
+    int before, b_lo, b_hi;
+    const int total = total_units<kJoinThreads>(w, warp_units, before, b_lo, b_hi);
+    const int n_cta = min((total + kJoin + kBlocks - 1) / (kJoin + kBlocks), kKv4Ctas);
+    const int c0 = blockIdx.x;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    const int lo = c0 < n_cta ? (int)((int64_t)total * c0 / n_cta) : 0, hi = c0 < n_cta ? (int)((int64_t)total * (c0 + 1) / n_cta) : 0;
+    for (int b = b_lo; b < b_hi; ++b) { // the segment of the slice's last unit
+        const int u = w.units(a.lens[b]), n = u * a.H_kv;
+        if (hi > before && hi <= before + n) {
+            const int r = (hi - 1 - before) / u, seg = before + r * u + kJoin;
+            if (seg >= lo && seg < hi && seg + u - kJoin > hi) {
+                found[0] = b;
+                found[1] = r;
+                found[2] = seg;
+                found[3] = u - kJoin;
             }
         }
-        sync_consumers(); // the join scratch is free again
+        before += n;
+    }
+    __syncthreads();
+    pdl_wait();
+    const int b = found[0], row = blockIdx.y * kJoinRows + warp / kJoinGroups, grp = warp % kJoinGroups, G = a.H_q / a.H_kv;
+    if (b < 0) return;
+    const int c1 = (int)(((int64_t)(found[2] + found[3]) * n_cta - 1) / total), np = c1 - c0 + 1;
+    // slot of CTA c: the segment is its slice's first unless the slice starts before it (only c0's can)
+    const float* parts = a.parts + (int64_t)2 * c0 * kKv4PartFloats;
+    const int first = found[2] > lo ? 1 : 0;
+    float M = -CUDART_INF_F, L = 0.f;
+    float4 acc = {};
+    if (row < G) {
+#pragma unroll 8
+        for (int c = grp; c < np; c += kJoinGroups) {
+            const float* p = parts + (int64_t)(c == 0 ? first : 2 * c) * kKv4PartFloats;
+            const float4 v = lane < L4 ? reinterpret_cast<const float4*>(p + row * DH)[lane] : float4{};
+            merge(M, L, acc, p[16 * 128 + row], p[16 * 128 + 16 + row], v);
+        }
+        if (lane < L4) sv[warp / kJoinGroups][grp][lane] = acc;
+        if (lane == 0) sml[warp / kJoinGroups][grp] = make_float2(M, L);
+    }
+    __syncthreads();
+    if (row < G && grp == 0 && lane < L4) {
+#pragma unroll
+        for (int i = 1; i < kJoinGroups; ++i) {
+            const float2 ml = sml[warp / kJoinGroups][i];
+            merge(M, L, acc, ml.x, ml.y, sv[warp / kJoinGroups][i][lane]);
+        }
+        finish(a, (int64_t)b * a.H_q + found[1] * G + row, lane * 4, acc, M, L);
     }
 }
 
@@ -699,7 +710,10 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
     int before, b_lo, b_hi;
     const int total = total_units<kWThreads>(w, warp_units, before, b_lo, b_hi);
     const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-    if (lo >= hi) return;
+    if (lo >= hi) {
+        pdl_wait();
+        return;
+    }
     for (int b = b_lo; b < b_hi; ++b) {
         const int n = w.units(a.lens[b]) * a.H_kv;
         if (lo >= before && lo < before + n) {
@@ -709,6 +723,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         before += n;
     }
     __syncthreads();
+    pdl_wait(); // for the lse
     const bool rest = !(a.w_in == a.w_out && a.decay == 1.f); // keys of other blocks change too
     Walk<false> cons;
     for (cons.begin(w, b0, seg0, lo, hi); cons.more(); cons.next_segment(w)) {
@@ -780,15 +795,24 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
     static SmemOptIn opt_in;
     if (cudaError_t e = opt_in.set(kv4_decode_kernel<DH, GIVEN>, Cfg<DH>::SMEM)) return e;
     trace_begin(s);
-    kv4_decode_kernel<DH, GIVEN><<<kKv4Ctas, kLaunch, Cfg<DH>::SMEM, s>>>(a);
+    const int smem = Cfg<DH>::SMEM;
+    // only kernels of one call overlap (a kernel before it may write the lengths, which are read at once)
+    cudaError_t e = cudaSuccess;
+    if (GIVEN && a.after_topk)
+        e = launch_pdl(kv4_decode_kernel<DH, GIVEN>, dim3(kKv4Ctas), kLaunch, smem, s, a);
+    else
+        kv4_decode_kernel<DH, GIVEN><<<kKv4Ctas, kLaunch, smem, s>>>(a);
+    if (e == cudaSuccess)
+        e = launch_pdl(kv4_join_kernel<DH, GIVEN>, dim3(kKv4Ctas, (a.H_q / a.H_kv + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, s, a);
     trace_end(s, MSA_KERNEL_KV4_ATTN);
-    note_launch(1);
-    if (!a.w_out) return cudaGetLastError();
-    trace_begin(s);
-    kv4_weights_kernel<DH, GIVEN><<<2 * kKv4Ctas, kWThreads, 0, s>>>(a);
-    note_launch(1);
-    trace_end(s, MSA_KERNEL_KV4_WEIGHTS);
-    return cudaGetLastError();
+    note_launch(2);
+    if (a.w_out && e == cudaSuccess) {
+        trace_begin(s);
+        e = launch_pdl(kv4_weights_kernel<DH, GIVEN>, dim3(2 * kKv4Ctas), kWThreads, 0, s, a);
+        trace_end(s, MSA_KERNEL_KV4_WEIGHTS);
+        note_launch(1);
+    }
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 } // namespace

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
     const int rank = cluster.block_rank(), size = cluster.num_blocks();
     const int seg = blockIdx.x / size, b = seg / a.H_kv; // (sequence, KV head)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
     const int len = a.lens[b];
     const bool bad = len < 0 || len > a.L_max;
     const int n = bad ? 0 : len, left = min(n, a.keep);
@@ -209,6 +210,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4EvictArgs a)
     constexpr int IN = kMoveRows * 16 / kMoveThreads;                 // index keys: at most 16 units per row
     __shared__ int src[kMoveRows];
     const int b = blockIdx.z, r = blockIdx.y, tid = threadIdx.x, i0 = blockIdx.x * kMoveRows;
+    pdl_wait();
     const int rows = min(kMoveRows, a.lens_to[b] - i0);
     if (rows <= 0) return;
     const int64_t seg = (int64_t)b * a.H_kv + r;
@@ -303,13 +305,10 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s)
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return e;
     const dim3 grid((a.keep + kMoveRows - 1) / kMoveRows, a.H_kv, a.B);
-    if (a.d_h == 128)
-        kv4_move_kernel<128><<<grid, kMoveThreads, 0, s>>>(a);
-    else
-        kv4_move_kernel<64><<<grid, kMoveThreads, 0, s>>>(a);
+    e = launch_pdl(a.d_h == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, grid, kMoveThreads, 0, s, a);
     trace_end(s, MSA_KERNEL_KV4_EVICT);
     note_launch(2);
-    return cudaGetLastError();
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 } // namespace msa

@@ -1124,14 +1124,11 @@ msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf16* v, in
     return cuda_status(e, "kv4 read launch");
 }
 
-// Workspace of the attention: error word and arrival counters (cleared by every call), partials, and
-// an lse for the weights when the caller wants none.
-static size_t kv4_attn_head_bytes() { return kErrBytes + align_up(kKv4Ctas * sizeof(int), 256); }
-
+// Workspace of the attention: error word, partials, and an lse for the weights when the caller wants none.
 size_t msa_kv4_decode_workspace_size(int B, int H_q)
 {
     if (B < 1 || H_q < 1) return 0;
-    return kv4_attn_head_bytes() + align_up((size_t)2 * kKv4Ctas * kKv4PartFloats * 4, 256) +
+    return kErrBytes + align_up((size_t)2 * kKv4Ctas * kKv4PartFloats * 4, 256) +
            align_up((size_t)B * H_q * 4, 256);
 }
 
@@ -1148,10 +1145,10 @@ static msa_status kv4_decode_check(const msa_kv4_cache* c, const void* q, const 
     return MSA_OK;
 }
 
-// Validated arguments; ws: kv4 part of the workspace, whose head the caller has cleared.
+// Validated arguments.
 static msa_status kv4_decode_run(const msa_kv4_cache* c, const msa_bf16* q, const int32_t* lens, int H_q,
                                  const int32_t* block_idx, int k, int min_len, const float* w_in, float* w_out, float decay,
-                                 msa_bf16* out, float* lse, uint8_t* ws, int* err, cudaStream_t s)
+                                 msa_bf16* out, float* lse, uint8_t* ws, bool after_topk, cudaStream_t s)
 {
     Kv4DecodeArgs a{};
     a.q = q;
@@ -1171,14 +1168,14 @@ static msa_status kv4_decode_run(const msa_kv4_cache* c, const msa_bf16* q, cons
     a.L_max = c->L_max;
     a.min_len = min_len;
     a.out = out;
-    a.arrived = (int*)(ws + kErrBytes);
-    a.parts = (float*)(ws + kv4_attn_head_bytes());
+    a.parts = (float*)(ws + kErrBytes);
     a.lse = lse;
     if (w_out && !lse) a.lse = (float*)((uint8_t*)a.parts + align_up((size_t)2 * kKv4Ctas * kKv4PartFloats * 4, 256));
     a.w_in = w_in;
     a.w_out = w_out;
     a.decay = decay;
-    a.err = err;
+    a.err = (int*)ws;
+    a.after_topk = after_topk;
     return cuda_status(launch_kv4_decode(a, s), "kv4 decode launch");
 }
 
@@ -1192,10 +1189,7 @@ msa_status msa_kv4_decode(const msa_kv4_cache* cache, const msa_bf16* q, const i
     if (workspace_bytes < msa_kv4_decode_workspace_size(cache->B, H_q)) return MSA_ERR_WORKSPACE;
     if (injected("msa_kv4_decode")) return MSA_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kv4_attn_head_bytes(), s), "clearing the error word"))
-        return st0;
-    return kv4_decode_run(cache, q, lens, H_q, block_idx, k, 0, w_in, w_out, decay, out, lse, (uint8_t*)workspace,
-                          (int*)workspace, s);
+    return kv4_decode_run(cache, q, lens, H_q, block_idx, k, 0, w_in, w_out, decay, out, lse, (uint8_t*)workspace, false, s);
 }
 
 size_t msa_sparse_decode_kv4_workspace_size(int B, int64_t L_max, int H_q, int H_kv, int B_k, int k)
@@ -1223,8 +1217,7 @@ msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_bf16* q, 
     if (injected("msa_sparse_decode_kv4")) return MSA_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     uint8_t* ws = (uint8_t*)workspace;
-    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kv4_attn_head_bytes(), s), "clearing the error word"))
-        return st0;
+    if (msa_status st0 = cuda_status(cudaMemsetAsync(workspace, 0, kErrBytes, s), "clearing the error word")) return st0;
     const int B = cache->B, H_kv = cache->H_kv;
     size_t off = msa_kv4_decode_workspace_size(B, H_q);
     DecodeArgs a{};
@@ -1248,7 +1241,7 @@ msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_bf16* q, 
     a.block_idx_out = block_idx_out;
     a.err = (int*)workspace;
     if (msa_status st = cuda_status(launch_decode_index(a, s), "decode index launch")) return st;
-    return kv4_decode_run(cache, q, lens, H_q, a.sel, k, 1, w_in, w_out, decay, out, lse, ws, (int*)workspace, s);
+    return kv4_decode_run(cache, q, lens, H_q, a.sel, k, 1, w_in, w_out, decay, out, lse, ws, true, s);
 }
 
 size_t msa_kv4_evict_workspace_size(int, int, int) { return kErrBytes; }

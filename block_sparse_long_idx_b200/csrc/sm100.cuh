@@ -315,13 +315,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-// Adds to a shared-memory word; orders the CTA's accesses before it and after it. Returns the old value.
-__device__ __forceinline__ int atom_add_acq_rel_cta(int* p, int v)
-{
-    int old;
-    asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(p)), "r"(v) : "memory");
-    return old;
-}
+// Programmatic dependent launch: let the next kernel of the stream start its CTAs once all of this one's have
+// called it or exited; wait for the previous kernel's completion (its writes visible). Both do nothing
+// where the kernels were not launched that way.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Orders this thread's shared-memory accesses before later bulk copies to the same memory.
 __device__ __forceinline__ void fence_proxy_async()
