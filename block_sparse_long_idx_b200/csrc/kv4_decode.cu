@@ -38,10 +38,11 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kLaunch = kThreads + 128; // and one warpgroup whose first thread starts the copies
 constexpr int kRegs = 160, kProducerRegs = 32; // of the 128 a thread is launched with
 static_assert(kThreads * kRegs + 128 * kProducerRegs <= kLaunch * 128, "register split");
-#ifndef KPAD
-#define KPAD 4
-#endif
-constexpr int kJoin = KPAD; // what joining a segment costs, in blocks: it counts in the split of the work
+// What joining a segment costs, in blocks: it counts in the split of the work. Measured with 3, 4, 6 and 8:
+// 24 ragged sequences of 8 heads of 64 take 31.9, 31.0, 28.6 and 28.1 us, one sequence with 16 given blocks
+// 18.2, 18.2, 19.9 and 21.9 us (fewer CTAs then).
+template <bool GIVEN>
+constexpr int kJoin = GIVEN ? 4 : 6;
 constexpr int kSlots = kWarps / 2; // join scratch: one output per pair of warps
 constexpr int kTile = 32;          // keys of a warp's part
 constexpr float kHeadroom = 7.f;   // P's reference: log2 units below the maximum it was set from
@@ -73,7 +74,7 @@ struct Work {
     __device__ __forceinline__ int units(int len) const // per segment
     {
         const int n = blocks(len);
-        return n > 0 ? n + kJoin : 0;
+        return n > 0 ? n + kJoin<GIVEN> : 0;
     }
     // First key of entry i of (b, r); -1 for padding and for entries the check reports.
     __device__ __forceinline__ int key0(int b, int r, int i, int len) const
@@ -136,14 +137,14 @@ struct Walk {
         b = b0;
         len = w.a.lens[b];
         n = w.blocks(len);
-        r = (lo - seq0) / (n + kJoin);
-        seg = seq0 + r * (n + kJoin) + kJoin;
+        r = (lo - seq0) / (n + kJoin<GIVEN>);
+        seg = seq0 + r * (n + kJoin<GIVEN>) + kJoin<GIVEN>;
         enter();
     }
     __device__ __forceinline__ bool more() const { return seg < hi; }
     __device__ __forceinline__ void next_segment(const Work<GIVEN>& w)
     {
-        seg += n + kJoin;
+        seg += n + kJoin<GIVEN>;
         if (++r == w.a.H_kv) {
             r = 0;
             if (seg < hi) { // the list goes on
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
     }
     int before, b_lo, b_hi;
     const int total = total_units<kLaunch>(w, sh.warp_units, before, b_lo, b_hi);
-    const int n_cta = min((total + kJoin + kBlocks - 1) / (kJoin + kBlocks), (int)gridDim.x); // a chunk or more for each
+    const int n_cta = min((total + kJoin<GIVEN> + kBlocks - 1) / (kJoin<GIVEN> + kBlocks), (int)gridDim.x); // a chunk or more for each
     const int cta = blockIdx.x;
     // sequences without keys have no units: the last CTA answers for them, and reports what is rejected
     pdl_trigger();
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeArgs a)
     const Work<GIVEN> w{a};
     int before, b_lo, b_hi;
     const int total = total_units<kJoinThreads>(w, warp_units, before, b_lo, b_hi);
-    const int n_cta = min((total + kJoin + kBlocks - 1) / (kJoin + kBlocks), kKv4Ctas);
+    const int n_cta = min((total + kJoin<GIVEN> + kBlocks - 1) / (kJoin<GIVEN> + kBlocks), kKv4Ctas);
     const int c0 = blockIdx.x;
     if (tid == 0) found[0] = -1;
     __syncthreads();
@@ -653,12 +654,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeArgs a)
     for (int b = b_lo; b < b_hi; ++b) { // the segment of the slice's last unit
         const int u = w.units(a.lens[b]), n = u * a.H_kv;
         if (hi > before && hi <= before + n) {
-            const int r = (hi - 1 - before) / u, seg = before + r * u + kJoin;
-            if (seg >= lo && seg < hi && seg + u - kJoin > hi) {
+            const int r = (hi - 1 - before) / u, seg = before + r * u + kJoin<GIVEN>;
+            if (seg >= lo && seg < hi && seg + u - kJoin<GIVEN> > hi) {
                 found[0] = b;
                 found[1] = r;
                 found[2] = seg;
-                found[3] = u - kJoin;
+                found[3] = u - kJoin<GIVEN>;
             }
         }
         before += n;
@@ -704,6 +705,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
 {
     using C = Cfg<DH>;
     __shared__ int warp_units[kWThreads / 32], b0, seg0;
+    __shared__ uint4 q[DH / 16][32]; // Q fragments of the segment
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.H_q / a.H_kv;
     const Work<false> w{a}; // all visible blocks
@@ -728,42 +730,47 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
     Walk<false> cons;
     for (cons.begin(w, b0, seg0, lo, hi); cons.more(); cons.next_segment(w)) {
         if (cons.pos >= cons.end) continue;
-        uint32_t qf[DH / 16][4];
         float f0, f1;
-        load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
-        auto qget = [&](int i, uint32_t (&v)[4]) { v[0] = qf[i][0], v[1] = qf[i][1], v[2] = qf[i][2], v[3] = qf[i][3]; };
+        __syncthreads(); // the segment before is done with q
+        {
+            uint32_t qf[DH / 16][4];
+            load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
+            if (warp == 0)
+                for (int i = 0; i < DH / 16; ++i) q[i][lane] = make_uint4(qf[i][0], qf[i][1], qf[i][2], qf[i][3]);
+        }
+        __syncthreads();
+        auto qget = [&](int i, uint32_t (&v)[4]) {
+            const uint4 u = lds128(&q[i][lane]);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+        };
         const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
         const float z0 = g < G ? lse[g] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
         const float z1 = g + 8 < G ? lse[g + 8] * 1.4426950408889634f : CUDART_INF_F;
         int mine = -1; // given blocks: the first key of this lane's
         if (GIVEN && lane < a.k) mine = Work<true>{a}.key0(cons.b, cons.r, lane, cons.len);
         const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
-        const int my_key = 8 * (g >> 1) + t + 4 * (g & 1);
-        // the next tile of this warp that has work: its rows and the lane's old weight are loaded one tile ahead
-        int next = 4 * cons.pos + warp;
-        struct Ahead {
+        const int my_key = 8 * (g >> 1) + t + 4 * (g & 1), last = min(cons.len, (cons.end - cons.seg) * kBk);
+        int next = (cons.pos - cons.seg) * kBk + warp * kTile; // first key of the warp's next tile
+        // a tile's rows and the lane's old weight are loaded one tile ahead
+        struct Tile {
             KTile<DH> k;
-            int64_t row; // first row, -1: none
-            int nk;
+            int key0; // first key; last or more: no tile
             bool chosen;
             float old;
-        } ahead;
-        auto fetch = [&] {
-            ahead.row = -1;
-            for (; next < 4 * cons.end && ahead.row < 0; next += kWThreads / 32) {
-                const int key0 = (next - 4 * cons.seg) * kTile;
-                ahead.nk = min(kTile, cons.len - key0);
-                ahead.chosen = !GIVEN || __any_sync(0xffffffffu, mine == key0 / kBk * kBk);
-                if (ahead.nk <= 0 || !(ahead.chosen || rest)) continue;
-                ahead.row = row0 + key0;
-                if (ahead.chosen) ahead.k.load(a.k_codes + ahead.row * C::CODE, a.k_scales + ahead.row * C::NG, g, t);
-                ahead.old = my_key < ahead.nk && a.w_in ? a.decay * a.w_in[ahead.row + my_key] : 0.f;
-            }
         };
-        fetch();
-        while (ahead.row >= 0) {
-            const Ahead now = ahead;
-            fetch();
+        auto fetch = [&](Tile& x) {
+            for (;; next += kWThreads) {
+                x.key0 = next;
+                if (next >= last) return;
+                x.chosen = !GIVEN || __any_sync(0xffffffffu, mine == next / kBk * kBk);
+                if (x.chosen || rest) break;
+            }
+            const int64_t row = row0 + next;
+            if (x.chosen) x.k.load(a.k_codes + row * C::CODE, a.k_scales + row * C::NG, g, t);
+            x.old = a.w_in && next + my_key < last ? a.decay * a.w_in[row + my_key] : 0.f;
+            next += kWThreads;
+        };
+        auto finish_tile = [&](const Tile& now) {
             float add = 0.f;
             if (now.chosen) {
                 float x[4][4];
@@ -784,7 +791,15 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
                 }
                 add = p[0];
             }
-            if (my_key < now.nk) a.w_out[now.row + my_key] = now.old + add;
+            if (now.key0 + my_key < last) a.w_out[row0 + now.key0 + my_key] = now.old + add;
+        };
+        Tile even, odd;
+        for (fetch(even); even.key0 < last;) {
+            fetch(odd);
+            finish_tile(even);
+            if (odd.key0 >= last) break;
+            fetch(even);
+            finish_tile(odd);
         }
     }
 }
