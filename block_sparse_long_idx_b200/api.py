@@ -519,12 +519,13 @@ def _tables(cache, T, starts, cu_seqlens):
 
 def _token_stride(t, name, cache):
     """Elements between the rows of t [T, H_kv, d_h], whose rows are contiguous."""
-    if (not t.is_cuda or t.device != cache.device or t.dtype not in _BF16 or t.dim() != 3 or
-            tuple(t.shape[1:]) != (cache.H_kv, cache.d_h) or t.stride(2) != 1 or
-            (cache.H_kv > 1 and t.stride(1) != cache.d_h)):
+    T, H, d = t.shape if t.dim() == 3 else (0, 0, 0)
+    strides = t.stride()
+    if (H != cache.H_kv or d != cache.d_h or strides[2] != 1 or (H > 1 and strides[1] != d) or t.dtype not in _BF16 or
+            t.device != cache.device or not t.is_cuda):
         raise ValueError(f"{name}: expected a 16-bit tensor [T, {cache.H_kv}, {cache.d_h}] on {cache.device} whose rows are "
                          f"contiguous, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else cache.H_kv * cache.d_h
+    return strides[0] if T > 1 else H * d
 
 
 @_on_device
@@ -556,7 +557,7 @@ def msa_kv4_read(cache: KV4Cache, starts, cu_seqlens=None, T: int | None = None,
     _tables(cache, T, starts, cu_seqlens)
     shape = (T, cache.H_kv, cache.d_h)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        k = torch.empty_strided(shape, (cache.H_kv * cache.d_h, cache.d_h, 1), dtype=torch.bfloat16, device=cache.device)
     else:
         _is(k, "k", _BF16, shape, cache.device)
     if v is None:
@@ -611,7 +612,7 @@ def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weigh
     if out is None:
         out = torch.empty_like(q)
     if lse is None and want_lse:
-        lse = torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device)
+        lse = torch.empty_strided((cache.B, H_q), (H_q, 1), dtype=torch.float32, device=cache.device)
     ws = _workspace(_kv4_decode_bytes(cache.B, H_q), cache.device, workspace)
     _check("msa_kv4_decode", lib.msa_kv4_decode(
         cache._ref, q.data_ptr(), lens.data_ptr(), H_q, _ptr(block_idx), k, _ptr(weights), _ptr(weights_out), decay,
