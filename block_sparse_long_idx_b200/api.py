@@ -506,7 +506,7 @@ def _hold(stream, *tensors):
         return
     for t in tensors:
         if t is not None:
-            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device))
+            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), t.device))
 
 
 def _tables(cache, T, starts, cu_seqlens):

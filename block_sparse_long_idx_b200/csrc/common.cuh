@@ -37,6 +37,24 @@ void trace_begin(cudaStream_t s);
 void trace_end(cudaStream_t s, int kernel_id);
 void note_launch(int n);
 
+// Launch whose CTAs may start before the stream's previous kernel has ended (they call pdl_wait() before
+// they read what it wrote; every CTA calls it, so that the launch ends after that kernel).
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ---------------------------------------------------------------------------------------------
 // launchers implemented in the .cu files
 // ---------------------------------------------------------------------------------------------

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(1024) decode_prefix_kernel(DecodeArgs a)
     __shared__ int64_t warp_sum[32];
     __shared__ int64_t carry;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
     if (tid == 0) {
         carry = 0;
         a.blk_prefix[0] = 0;
@@ -97,8 +98,7 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row_elems = (int64_t)a.H_kv * a.d_idx;
     const uint32_t blk_bytes = (uint32_t)(kBk * row_elems * 2);
-    const int64_t total = a.blk_prefix[a.B];
-    const int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
+    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPoolStages; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -108,6 +108,9 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
         fence_mbar_init();
     }
     __syncthreads();
+    pdl_wait(); // for the block prefix
+    const int64_t total = a.blk_prefix[a.B];
+    const int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
     if (g0 >= g1) return;
     volatile int* abort_flag = &sh.abort_flag;
     // the sequence holding block g0: the last beta with prefix[beta] <= g0
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
 // blocks at a time in registers, and draws its best k - 1 pairs one by one: each lane knows its best
 // remaining pair, two warp reductions find the best score and its lowest block, the owner looks for its
 // next. Rounds, and then the warps, pass on only those k - 1. (Per-lane insertion lists with a shuffle
-// merge took 31 us for 64 sequences in [16K, 128K] and 4 groups; this takes 9.)
+// merge took 31 us for 64 sequences in [16K, 128K] and 4 groups, traced; this takes 13.)
 constexpr int kTopkWarps = 4, kTopkPer = 8;
 
 // Integers that order like the scores (-0 and +0 are one value), 0 for none.
@@ -276,6 +279,7 @@ __global__ void __launch_bounds__(kTopkWarps * 32) decode_topk_kernel(DecodeArgs
     __shared__ int blks[kTopkWarps][kMaxK];
     const int beta = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
+    pdl_wait(); // for the pooled scores
     const int len = a.lens[beta];
     const int64_t seg = (int64_t)beta * a.H_kv + r;
     int32_t* sel = a.sel + seg * a.k;
@@ -554,10 +558,12 @@ cudaError_t launch_decode_index(const DecodeArgs& a, cudaStream_t s)
     trace_begin(s);
     decode_prefix_kernel<<<1, 1024, 0, s>>>(a);
     // one CTA per SM, each an equal slice of the flattened block list
-    decode_pool_kernel<<<n_sm, (kPoolConsumers + 1) * 32, kPoolSmem, s>>>(a, nb_max);
+    e0 = launch_pdl(decode_pool_kernel, dim3(n_sm), (kPoolConsumers + 1) * 32, kPoolSmem, s, a, nb_max);
+    if (e0 != cudaSuccess) return e0;
     trace_end(s, MSA_KERNEL_DEC_POOL);
     trace_begin(s);
-    decode_topk_kernel<<<dim3(a.B, a.H_kv), kTopkWarps * 32, 0, s>>>(a, nb_max);
+    e0 = launch_pdl(decode_topk_kernel, dim3(a.B, a.H_kv), kTopkWarps * 32, 0, s, a, nb_max);
+    if (e0 != cudaSuccess) return e0;
     trace_end(s, MSA_KERNEL_DEC_TOPK);
     note_launch(3);
     return cudaGetLastError();

@@ -96,24 +96,6 @@ public:
     }
 };
 
-// Launch whose CTAs may start before the stream's previous kernel has ended (they call pdl_wait() before
-// they read what it wrote; every CTA calls it, so that the launch ends after that kernel).
-template <class... P, class... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
 // Rows of a packed batch: row i of T belongs to the sequence b with cu[b] <= i < cu[b + 1] (cu =
 // nullptr: one row per sequence) and to position starts[b] + i - cu[b] of its cache.
 struct Kv4RowsArgs {

@@ -41,7 +41,7 @@ struct SelShared {
     int sums[2][kBins]; // of the CTA's copies, read by the cluster
     int tmp[kSelWarps];
     uint32_t prefix; // of the key looked for, and how many of its equals are still to be taken
-    int need;
+    int need, whole;
     int ties[kSelWarps], takes[kSelWarps];
     int cta_ties, cta_sure; // this CTA's equal keys, and tokens kept without a choice
 };
@@ -140,14 +140,18 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 if (before < need && before + count[u] >= need) { // one bin of one thread
-                    sh.prefix = T | ((uint32_t)(top + PER - 1 - u) << shift);
-                    sh.need = need - before;
+                    const uint32_t prefix = T | ((uint32_t)(top + PER - 1 - u) << shift);
+                    // a bin that is taken whole: its keys are those above prefix - 1, and no further digit is needed
+                    sh.whole = before + count[u] == need && prefix != 0u;
+                    sh.prefix = sh.whole ? prefix - 1u : prefix;
+                    sh.need = sh.whole ? 0 : need - before;
                 }
                 before += count[u];
             }
             __syncthreads();
             T = sh.prefix;
             need = sh.need;
+            if (sh.whole) break; // the same in the whole cluster
         }
     }
     // ---------------------------------------------------------------- kept positions in order

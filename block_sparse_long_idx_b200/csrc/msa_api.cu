@@ -1074,7 +1074,7 @@ static msa_status kv4_rows_check(const msa_kv4_cache* c, const void* k, const vo
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(cu, 4) || !aligned(workspace, 256) ||
         (!cu && T != c->B))
         return MSA_ERR_INVALID_ARG;
-    if (T > kv4_rows(c)) return MSA_ERR_INVALID_ARG; // more rows than the cache has
+    if (T > c->B * c->L_max) return MSA_ERR_INVALID_ARG; // more rows than the cache has
     if (workspace && workspace_bytes < kErrBytes) return MSA_ERR_WORKSPACE;
     return MSA_OK;
 }

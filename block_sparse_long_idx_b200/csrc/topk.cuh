@@ -107,50 +107,4 @@ __device__ __forceinline__ void emit_selection(const TopkList& t, int local, int
         if (j < k) out[j] = sel[j] == 0x7FFFFFFF ? -1 : sel[j];
 }
 
-// Warp-shuffle merge of 32 per-lane lists into the warp's best k-1 (same order), returned in
-// lane-uniform arrays best_v/best_b (entries past the found ones are (-inf, INT_MAX)).
-// Each round every lane exposes its best remaining entry, a butterfly reduction finds the
-// overall winner, and the owning lane pops it.
-__device__ __forceinline__ void warp_merge(TopkList& t, int k_keep, float (&best_v)[kMaxK - 1],
-                                           int (&best_b)[kMaxK - 1])
-{
-    const int lane = threadIdx.x & 31;
-    int head = TopkList::L - k_keep; // first real slot of this lane's list
-#pragma unroll
-    for (int j = 0; j < TopkList::L; ++j) {
-        best_v[j] = -CUDART_INF_F;
-        best_b[j] = 0x7FFFFFFF;
-    }
-    for (int round = 0; round < k_keep; ++round) {
-        float hv = -CUDART_INF_F;
-        int hb = 0x7FFFFFFF;
-#pragma unroll
-        for (int j = 0; j < TopkList::L; ++j)
-            if (j == head) {
-                hv = t.v[j];
-                hb = t.b[j];
-            }
-        float wv = hv;
-        int wb = hb, wl = lane;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, wv, off);
-            const int ob = __shfl_xor_sync(0xffffffffu, wb, off);
-            const int ol = __shfl_xor_sync(0xffffffffu, wl, off);
-            if (beats(ov, ob, wv, wb) || (ov == wv && ob == wb && ol < wl)) {
-                wv = ov;
-                wb = ob;
-                wl = ol;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < TopkList::L; ++j)
-            if (j == round) {
-                best_v[j] = wv;
-                best_b[j] = wb;
-            }
-        if (lane == wl) ++head;
-    }
-}
-
 } // namespace msa

@@ -332,6 +332,31 @@ def test_sparse_decode(shape):
     check_decode(c, q, bad, o2, l2, s2.cpu().numpy(), seqs=[1, 3, 4, 5])  # split otherwise than above: the same to rounding
 
 
+@pytest.mark.parametrize("k", [1, 2, 16])
+def test_sparse_selection_long(k):
+    """Top-k over rows of more blocks than a round of the selection holds, of many equal scores, and of one block;
+    with one block to choose it is the local one. Outputs and weights (none before) are those of the blocks."""
+    H, d, d_idx, G = 1, 64, 32, 2
+    lens = [140001, 140000 - 128, 1, 40000]
+    B, L_max = len(lens), 140032
+    c = fill_cache(B, L_max, H, d, lens, seed=40 + k)
+    g = torch.Generator("cuda").manual_seed(41)
+    q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
+    q_idx = torch.randint(-3, 4, (B, H, d_idx), device="cuda", generator=g).bfloat16()
+    k_idx = torch.randint(-1, 2, (B, L_max, H, d_idx), device="cuda", generator=g).bfloat16()
+    q_idx[1] = 0                                     # all scores equal, zeros
+    w_out = torch.full((B, H, L_max), 4.0, device="cuda")
+    out, lse, sel = msa.msa_sparse_decode_kv4(q, q_idx, c, k_idx, i32(lens), 128, k, weights_out=w_out)
+    for b, n in enumerate(lens):
+        local = (n - 1) // 128
+        s = (k_idx[b, :local * 128, 0].double() @ q_idx[b, 0].double()).view(local, 128).amax(-1).cpu().numpy() if local else np.zeros(0)
+        best = np.lexsort((np.arange(local), -s))[:k - 1]
+        want = np.full(k, -1)
+        want[:len(best) + 1] = np.sort(np.append(best, local))
+        assert sel[b, 0].tolist() == want.tolist(), b
+    check_decode(c, q, lens, out, lse, sel.cpu().numpy(), None, w_out, torch.full_like(w_out, 4.0))
+
+
 # ------------------------------------------------------------------------------------------ eviction
 def check_evict(c, to, w, lens, keep, recent, first, k_idx, fill):
     H, d_idx = c.H_kv, k_idx.shape[-1]
@@ -373,7 +398,7 @@ def test_evict(case):
     check_evict(c, to, w, lens, keep, recent, first, k_idx, 0x3C)
 
 
-@pytest.mark.parametrize("n", [16385, 100003])
+@pytest.mark.parametrize("n", [16385, 100003, 150001])
 def test_evict_long(n):
     """Long sequences, weights as attention leaves them (a few heavy ones, most of one magnitude)."""
     H, d, keep = 2, 64, n // 5

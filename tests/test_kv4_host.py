@@ -76,7 +76,7 @@ def test_rows_validation(msa):
     assert app(k=None) == INVALID and app(v=P2 + 2) == INVALID and app(starts=None) == INVALID
     assert app(ks=255) == INVALID and app(ks=248) == INVALID and app(vs=260) == INVALID   # below a row; not a multiple of 8
     assert app(T=-1) == INVALID and app(cu=None) == INVALID                                # T rows need T = B without tables
-    assert app(T=4 * 2 * 1024 + 1) == INVALID                                              # more rows than the cache has
+    assert app(T=4 * 1024 + 1) == INVALID                                                  # more rows than the cache has
     assert app(cu=P2 + 2) == INVALID and app(ws=WS + 16) == INVALID
     assert app(n=need - 1) == WORKSPACE
     rd = caller(msa.lib.msa_kv4_read, ["cache", "k", "v", "T", "starts", "cu", "ws", "n", "stream"],
