@@ -169,15 +169,16 @@ struct Shared {
     int abort_flag;
 };
 
-// A fragments of q's rows g and g + 8 (rows past the G heads are zero) in fp16, and the factors that
-// turn sums of the products into logits in log2 units.
-template <int DH>
+// Fragments of q's rows g and g + 8 (rows past the G heads are zero) in fp16, and the factors that turn sums of
+// the products into logits in log2 units, of the two heads that the lane's scores belong to (rows_of below).
+// NARROW: of row g only; qf[i][0], [2] are then the B fragment of step i.
+template <int DH, bool NARROW>
 __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int G, int g, int t, uint32_t (&qf)[DH / 16][4],
                                        float& f0, float& f1)
 {
     const float base = a.k_scale * rsqrtf((float)DH) * 1.4426950408889634f;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < (NARROW ? 1 : 2); ++half) {
         const int row = g + 8 * half;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * a.H_q + r * G + row) * DH + t * (DH / 4));
         uint32_t x[DH / 8];
@@ -198,6 +199,24 @@ __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int
 #pragma unroll
         for (int i = 0; i < DH / 8; ++i) // pair i: elements 2 i, 2 i + 1 of the lane's run
             qf[i / 2][2 * (i & 1) + half] = pack_f16x2(bf16_lo(x[i]) * down, bf16_hi(x[i]) * down);
+    }
+    if (NARROW) {
+        const float f = f0;
+        f0 = __shfl_sync(0xffffffffu, f, 8 * t);
+        f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+    }
+}
+
+// Q fragments of a segment in shared memory: 16 bytes a lane, one step's A fragment, or two steps' B fragments.
+template <int DH, bool NARROW>
+__device__ __forceinline__ void store_q(uint4 (*q)[32], const uint32_t (&qf)[DH / 16][4], int lane)
+{
+    if constexpr (NARROW) {
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) q[i][lane] = make_uint4(qf[2 * i][0], qf[2 * i][2], qf[2 * i + 1][0], qf[2 * i + 1][2]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i) q[i][lane] = make_uint4(qf[i][0], qf[i][1], qf[i][2], qf[i][3]);
     }
 }
 
@@ -226,10 +245,18 @@ struct KTile {
     }
 };
 
-// x[n][e] = the fp32 sums of q's rows (e < 2: g, else g + 8) with key 8 n + t + 4 (e & 1) of the tile.
-// qget(i, a): the A fragment of step i.
-template <int DH, class Q>
-__device__ __forceinline__ void scores(const KTile<DH>& k, const Q& qget, float (&x)[4][4])
+__device__ __forceinline__ uint4 lds128(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)));
+    return v;
+}
+
+// The fp32 sums of q's rows with the 32 keys of the tile, q as store_q left it.
+//   x[n][e]         : row g (e < 2) or g + 8, key 8 n + t + 4 (e & 1)
+//   NARROW, x[m][e] : row 2 t + (e & 1), key 16 m + 8 (e >> 1) + g / 2 + 4 (g % 2)
+template <int DH, bool NARROW>
+__device__ __forceinline__ void scores(const KTile<DH>& k, const uint4 (*q)[32], int lane, float (&x)[NARROW ? 2 : 4][4])
 {
     uint32_t s[4][DH / 64];
 #pragma unroll
@@ -237,30 +264,45 @@ __device__ __forceinline__ void scores(const KTile<DH>& k, const Q& qget, float 
         const uint32_t sc = e4m3x2_to_f16x2(k.s[n]);
         s[n][0] = prmt(sc, sc, 0x1010);
         if constexpr (DH == 128) s[n][1] = prmt(sc, sc, 0x3232);
+    }
+#pragma unroll
+    for (int n = 0; n < (NARROW ? 2 : 4); ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-    }
 #pragma unroll
     for (int i = 0; i < DH / 32; ++i) {
-        uint32_t h[4][4], qa[4], qb[4];
-        qget(2 * i, qa);
-        qget(2 * i + 1, qb);
+        uint32_t h[4][4];
+        if constexpr (NARROW) {
+            const uint4 v = lds128(&q[i][lane]);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            e2m1x8_to_f16x2(k.c[n][i], h[n]);
-            mma_f16_16816(x[n], qa, mul_f16x2(h[n][0], s[n][i / 2]), mul_f16x2(h[n][1], s[n][i / 2]));
+            for (int n = 0; n < 4; ++n) {
+                e2m1x8_to_f16x2(k.c[n][i], h[n]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[n][e] = mul_f16x2(h[n][e], s[n][i / 2]);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t a0[4] = {h[2 * m][0], h[2 * m + 1][0], h[2 * m][1], h[2 * m + 1][1]};
+                mma_f16_16816(x[m], a0, v.x, v.y);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t a1[4] = {h[2 * m][2], h[2 * m + 1][2], h[2 * m][3], h[2 * m + 1][3]};
+                mma_f16_16816(x[m], a1, v.z, v.w);
+            }
+        } else {
+            const uint4 va = lds128(&q[2 * i][lane]), vb = lds128(&q[2 * i + 1][lane]);
+            const uint32_t qa[4] = {va.x, va.y, va.z, va.w}, qb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                e2m1x8_to_f16x2(k.c[n][i], h[n]);
+                mma_f16_16816(x[n], qa, mul_f16x2(h[n][0], s[n][i / 2]), mul_f16x2(h[n][1], s[n][i / 2]));
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                mma_f16_16816(x[n], qb, mul_f16x2(h[n][2], s[n][i / 2]), mul_f16x2(h[n][3], s[n][i / 2]));
         }
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-            mma_f16_16816(x[n], qb, mul_f16x2(h[n][2], s[n][i / 2]), mul_f16x2(h[n][3], s[n][i / 2]));
     }
-}
-
-__device__ __forceinline__ uint4 lds128(const uint4* p)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)));
-    return v;
 }
 
 // ex2(-inf) = 0 keeps empty rows and tiles out of the joins.
@@ -290,12 +332,11 @@ __device__ __forceinline__ void finish(const Kv4DecodeArgs& a, int64_t row, int 
 // The consumers' barrier (the producer's warpgroup takes no part).
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
-template <int DH, bool GIVEN>
+template <int DH, bool GIVEN, bool NARROW>
 __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
 {
     using C = Cfg<DH>;
-    constexpr int KS = DH / 16; // contraction steps of S
-    constexpr int NT = DH / 8;  // output tiles of O
+    constexpr int NT = DH / 8; // elements of V's rows a lane reads
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
     float* join = reinterpret_cast<float*>(ring + kStages * C::STAGE);
@@ -413,23 +454,22 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
     bool ok = true;
     for (; cons.more(); cons.next_segment(w)) {
         if (cons.pos >= cons.end) continue;
-        uint32_t qf[KS][4];
         float f0, f1;
-        load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
-        if (warp == 0)
-            for (int i = 0; i < KS; ++i) sh.q[i][lane] = make_uint4(qf[i][0], qf[i][1], qf[i][2], qf[i][3]);
+        {
+            uint32_t qf[DH / 16][4];
+            load_q<DH, NARROW>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
+            if (warp == 0) store_q<DH, NARROW>(sh.q, qf, lane);
+        }
         sync_consumers();
-        auto qget = [&](int i, uint32_t (&v)[4]) {
-            const uint4 u = lds128(&sh.q[i][lane]);
-            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-        };
-        float o[NT][4];
+        // outputs: o[n][2 h + c], of head g + 8 h and element (2 t + c) NT + n; NARROW: o[i][2 u + h], of head 2 t + h
+        // and element g NT + 2 i + u
+        float o[NARROW ? NT / 2 : NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < (NARROW ? NT / 2 : NT); ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F; // references
-        uint64_t l0 = 0, l1 = 0;                      // this lane's sums, as pairs of even and odd columns
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F; // references of the lane's two heads
+        uint64_t l0 = 0, l1 = 0;                      // this lane's sums: of each head over even and odd columns; NARROW: l0, of both heads
 
         for (; ok && cons.pos < cons.end; cons.pos += kBlocks, ++used) {
             const uint32_t st = used % kStages;
@@ -446,38 +486,47 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 continue;
             }
             const uint8_t* s = ring + st * C::STAGE;
-            float x[4][4];
+            float x[NARROW ? 2 : 4][4];
             {
                 KTile<DH> k;
                 k.load(s + C::K_CODES + warp * kTile * C::CODE, s + C::K_SCALES + warp * kTile * C::NG, g, t);
-                scores<DH>(k, qget, x);
+                scores<DH, NARROW>(k, sh.q, lane, x);
             }
             const uint8_t* vc = s + C::V_CODES + warp * kTile * C::CODE;
             uint8_t* vs = ring + st * C::STAGE + C::V_SCALES + warp * kTile * C::NG;
             // ------------------------------------------------------------ softmax
             if (nk < kTile) { // the last tile of a segment
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 4; ++n) {
+                    if constexpr (NARROW) {
+                        const int m = n >> 1, u = n & 1;
+                        if (8 * n + (g >> 1) + 4 * (g & 1) >= nk) x[m][2 * u] = x[m][2 * u + 1] = -CUDART_INF_F;
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (8 * n + t + 4 * e >= nk) x[n][e] = x[n][2 + e] = -CUDART_INF_F;
+                        for (int e = 0; e < 2; ++e)
+                            if (8 * n + t + 4 * e >= nk) x[n][e] = x[n][2 + e] = -CUDART_INF_F;
+                    }
+                }
                 // rows past the length hold anything, NaN scales among it: they weigh 0 and must be finite
                 if (lane >= nk)
                     for (int i = 0; i < C::NG; i += 4) *reinterpret_cast<uint32_t*>(vs + lane * C::NG + i) = 0u;
                 __syncwarp();
                 fence_proxy_async(); // the stage is written by a bulk copy again
             }
-            float mx0 = max3f(x[0][0], x[0][1], x[1][0]), mx1 = max3f(x[0][2], x[0][3], x[1][2]);
-            mx0 = max3f(mx0, x[1][1], x[2][0]);
-            mx1 = max3f(mx1, x[1][3], x[2][2]);
-            mx0 = max3f(mx0, x[2][1], x[3][0]);
-            mx1 = max3f(mx1, x[2][3], x[3][2]);
-            mx0 = fmaxf(mx0, x[3][1]);
-            mx1 = fmaxf(mx1, x[3][3]);
-            // the references (equal in the 4 lanes of a row) move up only when P would leave [0, 2^15): exact, and rare
+            float mx0, mx1;
+            if constexpr (NARROW) {
+                mx0 = fmaxf(max3f(x[0][0], x[0][2], x[1][0]), x[1][2]);
+                mx1 = fmaxf(max3f(x[0][1], x[0][3], x[1][1]), x[1][3]);
+            } else {
+                mx0 = max3f(x[0][0], x[0][1], x[1][0]), mx1 = max3f(x[0][2], x[0][3], x[1][2]);
+                mx0 = max3f(mx0, x[1][1], x[2][0]), mx1 = max3f(mx1, x[1][3], x[2][2]);
+                mx0 = max3f(mx0, x[2][1], x[3][0]), mx1 = max3f(mx1, x[2][3], x[3][2]);
+                mx0 = fmaxf(mx0, x[3][1]), mx1 = fmaxf(mx1, x[3][3]);
+            }
+            // the references (equal in the lanes of a head) move up only when P would leave [0, 2^15): exact, and rare
             if (__any_sync(0xffffffffu, mx0 * f0 > m0 + kRaise || mx1 * f1 > m1 + kRaise)) { // f > 0
 #pragma unroll
-                for (int d = 1; d < 4; d <<= 1) {
+                for (int d = NARROW ? 4 : 1; d < (NARROW ? 32 : 4); d <<= 1) {
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
                 }
@@ -487,27 +536,39 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 const float r0 = join_weight(m0, n0), r1 = join_weight(m1, n1);
                 m0 = n0;
                 m1 = n1;
-                l0 = f2_mul(l0, f2_pack(r0, r0));
+                l0 = f2_mul(l0, f2_pack(r0, NARROW ? r1 : r0));
                 l1 = f2_mul(l1, f2_pack(r1, r1));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < (NARROW ? NT / 2 : NT); ++n) {
                     o[n][0] *= r0;
-                    o[n][1] *= r0;
-                    o[n][2] *= r1;
+                    o[n][1] *= NARROW ? r1 : r0;
+                    o[n][2] *= NARROW ? r0 : r1;
                     o[n][3] *= r1;
                 }
             }
+            // P in fp16: A fragments of 16 keys; NARROW: B fragments (keys by heads), from 8 x 8 transposes
             uint32_t pf[2][4];
-            const uint64_t ff0 = f2_pack(f0, f0), ff1 = f2_pack(f1, f1), mm0 = f2_pack(-m0, -m0), mm1 = f2_pack(-m1, -m1);
+            if constexpr (NARROW) {
+                const uint64_t ff = f2_pack(f0, f1), mm = f2_pack(-m0, -m1);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const uint64_t y0 = f2_fma(f2_pack(x[n][0], x[n][1]), ff0, mm0), y1 = f2_fma(f2_pack(x[n][2], x[n][3]), ff1, mm1);
-                const float p0 = ex2_approx(f2_lo(y0)), p1 = ex2_approx(f2_hi(y0));
-                const float p2 = ex2_approx(f2_lo(y1)), p3 = ex2_approx(f2_hi(y1));
-                l0 = f2_add(l0, f2_pack(p0, p1));
-                l1 = f2_add(l1, f2_pack(p2, p3));
-                pf[n >> 1][(n & 1) * 2] = pack_f16x2(p0, p1);
-                pf[n >> 1][(n & 1) * 2 + 1] = pack_f16x2(p2, p3);
+                for (int n = 0; n < 4; ++n) {
+                    const uint64_t y = f2_fma(f2_pack(x[n >> 1][2 * (n & 1)], x[n >> 1][2 * (n & 1) + 1]), ff, mm);
+                    const float p0 = ex2_approx(f2_lo(y)), p1 = ex2_approx(f2_hi(y));
+                    l0 = f2_add(l0, f2_pack(p0, p1));
+                    pf[n >> 1][n & 1] = transpose_8x8(pack_f16x2(p0, p1));
+                }
+            } else {
+                const uint64_t ff0 = f2_pack(f0, f0), ff1 = f2_pack(f1, f1), mm0 = f2_pack(-m0, -m0), mm1 = f2_pack(-m1, -m1);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint64_t y0 = f2_fma(f2_pack(x[n][0], x[n][1]), ff0, mm0), y1 = f2_fma(f2_pack(x[n][2], x[n][3]), ff1, mm1);
+                    const float p0 = ex2_approx(f2_lo(y0)), p1 = ex2_approx(f2_hi(y0));
+                    const float p2 = ex2_approx(f2_lo(y1)), p3 = ex2_approx(f2_hi(y1));
+                    l0 = f2_add(l0, f2_pack(p0, p1));
+                    l1 = f2_add(l1, f2_pack(p2, p3));
+                    pf[n >> 1][(n & 1) * 2] = pack_f16x2(p0, p1);
+                    pf[n >> 1][(n & 1) * 2 + 1] = pack_f16x2(p2, p3);
+                }
             }
             // ------------------------------------------------------------ O += P V, 16 keys a step
 #pragma unroll
@@ -538,59 +599,73 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                     e2m1x8_to_f16x2(((wv[0][i] >> 4) & 0x0F0F0F0Fu) | (wv[1][i] & 0xF0F0F0F0u), b0[1]);
                     e2m1x8_to_f16x2((wv[2][i] & 0x0F0F0F0Fu) | ((wv[3][i] << 4) & 0xF0F0F0F0u), b1[0]);
                     e2m1x8_to_f16x2(((wv[2][i] >> 4) & 0x0F0F0F0Fu) | (wv[3][i] & 0xF0F0F0F0u), b1[1]);
+                    if constexpr (NARROW) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        mma_f16_16816(o[8 * i + e], pf[j], mul_f16x2(b0[e & 1][e >> 1], sc[0]),
-                                      mul_f16x2(b1[e & 1][e >> 1], sc[1]));
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t va[4] = {mul_f16x2(b0[0][e], sc[0]), mul_f16x2(b0[1][e], sc[0]), mul_f16x2(b1[0][e], sc[1]),
+                                                    mul_f16x2(b1[1][e], sc[1])};
+                            mma_f16_16816(o[4 * i + e], va, pf[j][0], pf[j][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            mma_f16_16816(o[8 * i + e], pf[j], mul_f16x2(b0[e & 1][e >> 1], sc[0]),
+                                          mul_f16x2(b1[e & 1][e >> 1], sc[1]));
+                    }
                 }
             }
             leave(st);
         }
         // ------------------------------------------------------------ join the warps
-        float s0 = f2_lo(l0) + f2_hi(l0), s1 = f2_lo(l1) + f2_hi(l1);
+        float s0 = NARROW ? f2_lo(l0) : f2_lo(l0) + f2_hi(l0), s1 = NARROW ? f2_hi(l0) : f2_lo(l1) + f2_hi(l1);
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
+        for (int d = NARROW ? 4 : 1; d < (NARROW ? 32 : 4); d <<= 1) {
             s0 += __shfl_xor_sync(0xffffffffu, s0, d);
             s1 += __shfl_xor_sync(0xffffffffu, s1, d);
         }
+        // the lane's two heads, and its run of their elements in the scratch
+        constexpr int RUN = NARROW ? NT : 2 * NT;
+        const int h0 = NARROW ? 2 * t : g, h1 = NARROW ? 2 * t + 1 : g + 8;
+        float* mine = join + (warp % kSlots) * C::WARP + (NARROW ? (g >> 1) * C::LANE + (g & 1) * NT : t * C::LANE);
+        auto at = [&](int h, int e) -> float& { // element e of the run of head h0 (h = 0) or h1
+            if constexpr (NARROW)
+                return o[e >> 1][2 * (e & 1) + h];
+            else
+                return o[e % NT][2 * h + e / NT];
+        };
         // two steps: the upper half of the warps hand theirs to the lower half
-        float* mine = join + (warp % kSlots) * C::WARP + t * C::LANE;
         auto put = [&] {
-            if (t == 0) {
-                sh.m[warp % kSlots][g] = m0;
-                sh.m[warp % kSlots][g + 8] = m1;
-                sh.l[warp % kSlots][g] = s0;
-                sh.l[warp % kSlots][g + 8] = s1;
+            if (NARROW ? g == 0 : t == 0) {
+                sh.m[warp % kSlots][h0] = m0;
+                sh.m[warp % kSlots][h1] = m1;
+                sh.l[warp % kSlots][h0] = s0;
+                sh.l[warp % kSlots][h1] = s1;
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) // row g + 8 half: elements t * DH / 4 + (0 .. DH / 4)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int n = 0; n < NT; n += 4)
-                        *reinterpret_cast<float4*>(mine + (g + 8 * half) * C::ROW + c * NT + n) = make_float4(
-                            o[n][2 * half + c], o[n + 1][2 * half + c], o[n + 2][2 * half + c], o[n + 3][2 * half + c]);
+                for (int e = 0; e < RUN; e += 4)
+                    *reinterpret_cast<float4*>(mine + (h ? h1 : h0) * C::ROW + e) = make_float4(at(h, e), at(h, e + 1), at(h, e + 2), at(h, e + 3));
         };
         if (warp >= kSlots) put();
         sync_consumers();
         if (warp < kSlots) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float &m = half ? m1 : m0, &l = half ? s1 : s0;
-                const float om = sh.m[warp][g + 8 * half], M = fmaxf(m, om);
+            for (int h = 0; h < 2; ++h) {
+                float &m = h ? m1 : m0, &l = h ? s1 : s0;
+                const int row = h ? h1 : h0;
+                const float om = sh.m[warp][row], M = fmaxf(m, om);
                 const float wa = join_weight(m, M), wb = join_weight(om, M);
-                l = fmaf(wa, l, wb * sh.l[warp][g + 8 * half]);
+                l = fmaf(wa, l, wb * sh.l[warp][row]);
                 m = M;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int n = 0; n < NT; n += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(mine + (g + 8 * half) * C::ROW + c * NT + n);
-                        o[n][2 * half + c] = fmaf(wa, o[n][2 * half + c], wb * v.x);
-                        o[n + 1][2 * half + c] = fmaf(wa, o[n + 1][2 * half + c], wb * v.y);
-                        o[n + 2][2 * half + c] = fmaf(wa, o[n + 2][2 * half + c], wb * v.z);
-                        o[n + 3][2 * half + c] = fmaf(wa, o[n + 3][2 * half + c], wb * v.w);
-                    }
+                for (int e = 0; e < RUN; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(mine + row * C::ROW + e);
+                    at(h, e) = fmaf(wa, at(h, e), wb * v.x);
+                    at(h, e + 1) = fmaf(wa, at(h, e + 1), wb * v.y);
+                    at(h, e + 2) = fmaf(wa, at(h, e + 2), wb * v.z);
+                    at(h, e + 3) = fmaf(wa, at(h, e + 3), wb * v.w);
+                }
             }
             __syncwarp(); // every lane has read the rows' maxima and sums
             put();
@@ -700,7 +775,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeArgs a)
 // the keys of the others get decay * w_in alone.
 constexpr int kWThreads = 256;
 
-template <int DH, bool GIVEN>
+template <int DH, bool GIVEN, bool NARROW>
 __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs a)
 {
     using C = Cfg<DH>;
@@ -734,22 +809,19 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         __syncthreads(); // the segment before is done with q
         {
             uint32_t qf[DH / 16][4];
-            load_q<DH>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
-            if (warp == 0)
-                for (int i = 0; i < DH / 16; ++i) q[i][lane] = make_uint4(qf[i][0], qf[i][1], qf[i][2], qf[i][3]);
+            load_q<DH, NARROW>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
+            if (warp == 0) store_q<DH, NARROW>(q, qf, lane);
         }
         __syncthreads();
-        auto qget = [&](int i, uint32_t (&v)[4]) {
-            const uint4 u = lds128(&q[i][lane]);
-            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-        };
         const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
-        const float z0 = g < G ? lse[g] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
-        const float z1 = g + 8 < G ? lse[g + 8] * 1.4426950408889634f : CUDART_INF_F;
+        const int h0 = NARROW ? 2 * t : g, h1 = NARROW ? 2 * t + 1 : g + 8;
+        const float z0 = h0 < G ? lse[h0] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
+        const float z1 = h1 < G ? lse[h1] * 1.4426950408889634f : CUDART_INF_F;
         int mine = -1; // given blocks: the first key of this lane's
         if (GIVEN && lane < a.k) mine = Work<true>{a}.key0(cons.b, cons.r, lane, cons.len);
         const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
-        const int my_key = 8 * (g >> 1) + t + 4 * (g & 1), last = min(cons.len, (cons.end - cons.seg) * kBk);
+        // the key whose weight ends in this lane (of the sums below)
+        const int my_key = NARROW ? 8 * t + (g >> 1) + 4 * (g & 1) : 8 * (g >> 1) + t + 4 * (g & 1), last = min(cons.len, (cons.end - cons.seg) * kBk);
         int next = (cons.pos - cons.seg) * kBk + warp * kTile; // first key of the warp's next tile
         // a tile's rows and the lane's old weight are loaded one tile ahead
         struct Tile {
@@ -773,20 +845,23 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         auto finish_tile = [&](const Tile& now) {
             float add = 0.f;
             if (now.chosen) {
-                float x[4][4];
-                scores<DH>(now.k, qget, x);
-                // the heads' weights of key v = 2 n + e (the lane's columns): summed over the lanes g, which end with key g
-                float p[8];
+                float x[NARROW ? 2 : 4][4];
+                scores<DH, NARROW>(now.k, q, lane, x);
+                // the heads' weights of the lane's keys (v = 2 n + e, or 2 m + u), summed over the lanes that hold the key's
+                // other heads: these are as many as the keys, and each ends with one
+                constexpr int KEYS = NARROW ? 4 : 8;
+                float p[KEYS];
 #pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    p[v] = ex2_approx(fmaf(x[v >> 1][v & 1], f0, -z0)) + ex2_approx(fmaf(x[v >> 1][2 + (v & 1)], f1, -z1));
+                for (int v = 0; v < KEYS; ++v)
+                    p[v] = NARROW ? ex2_approx(fmaf(x[v >> 1][2 * (v & 1)], f0, -z0)) + ex2_approx(fmaf(x[v >> 1][2 * (v & 1) + 1], f1, -z1))
+                                  : ex2_approx(fmaf(x[v >> 1][v & 1], f0, -z0)) + ex2_approx(fmaf(x[v >> 1][2 + (v & 1)], f1, -z1));
 #pragma unroll
-                for (int half = 4; half > 0; half >>= 1) {
-                    const bool up = g & half;
+                for (int half = KEYS / 2; half > 0; half >>= 1) {
+                    const bool up = (NARROW ? t : g) & half;
 #pragma unroll
                     for (int v = 0; v < half; ++v) {
                         const float give = up ? p[v] : p[v + half], keep = up ? p[v + half] : p[v];
-                        p[v] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+                        p[v] = keep + __shfl_xor_sync(0xffffffffu, give, NARROW ? half : 4 * half);
                     }
                 }
                 add = p[0];
@@ -804,26 +879,26 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
     }
 }
 
-template <int DH, bool GIVEN>
+template <int DH, bool GIVEN, bool NARROW>
 cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
 {
     static SmemOptIn opt_in;
-    if (cudaError_t e = opt_in.set(kv4_decode_kernel<DH, GIVEN>, Cfg<DH>::SMEM)) return e;
+    if (cudaError_t e = opt_in.set(kv4_decode_kernel<DH, GIVEN, NARROW>, Cfg<DH>::SMEM)) return e;
     trace_begin(s);
     const int smem = Cfg<DH>::SMEM;
     // only kernels of one call overlap (a kernel before it may write the lengths, which are read at once)
     cudaError_t e = cudaSuccess;
     if (GIVEN && a.after_topk)
-        e = launch_pdl(kv4_decode_kernel<DH, GIVEN>, dim3(kKv4Ctas), kLaunch, smem, s, a);
+        e = launch_pdl(kv4_decode_kernel<DH, GIVEN, NARROW>, dim3(kKv4Ctas), kLaunch, smem, s, a);
     else
-        kv4_decode_kernel<DH, GIVEN><<<kKv4Ctas, kLaunch, smem, s>>>(a);
+        kv4_decode_kernel<DH, GIVEN, NARROW><<<kKv4Ctas, kLaunch, smem, s>>>(a);
     if (e == cudaSuccess)
         e = launch_pdl(kv4_join_kernel<DH, GIVEN>, dim3(kKv4Ctas, (a.H_q / a.H_kv + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, s, a);
     trace_end(s, MSA_KERNEL_KV4_ATTN);
     note_launch(2);
     if (a.w_out && e == cudaSuccess) {
         trace_begin(s);
-        e = launch_pdl(kv4_weights_kernel<DH, GIVEN>, dim3(2 * kKv4Ctas), kWThreads, 0, s, a);
+        e = launch_pdl(kv4_weights_kernel<DH, GIVEN, NARROW>, dim3(2 * kKv4Ctas), kWThreads, 0, s, a);
         trace_end(s, MSA_KERNEL_KV4_WEIGHTS);
         note_launch(1);
     }
@@ -834,8 +909,16 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s)
 {
-    if (a.block_idx) return a.d_h == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
-    return a.d_h == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
+    // up to 8 heads a KV head: keys are the rows of the products and heads the 8 columns, half the tensor-core
+    // work of 16 rows that are mostly padding. 16 sequences in [8K, 16K] of 8 KV heads of 128 take 50 us with 1
+    // head each, 51 with 8 and 68 with 16; with 16 rows for all 61, 63 and 68.
+    const bool narrow = a.H_q / a.H_kv <= 8, given = a.block_idx != nullptr;
+    if (a.d_h == 128) {
+        if (given) return narrow ? launch<128, true, true>(a, s) : launch<128, true, false>(a, s);
+        return narrow ? launch<128, false, true>(a, s) : launch<128, false, false>(a, s);
+    }
+    if (given) return narrow ? launch<64, true, true>(a, s) : launch<64, true, false>(a, s);
+    return narrow ? launch<64, false, true>(a, s) : launch<64, false, false>(a, s);
 }
 
 } // namespace msa

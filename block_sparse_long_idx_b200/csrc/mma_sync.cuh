@@ -33,6 +33,14 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// An 8 x 8 b16 matrix held as row lane / 4, columns 2 (lane % 4), + 1, transposed in the same layout.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // Four 8x8 b16 matrices; lanes 8i .. 8i+7 give the row addresses of matrix i, which lands in ri.
 // For an A fragment of a row-major 16 x 16 block at p0 (row stride ld): lane address
 // p0 + (lane % 16) * ld + (lane / 16) * 8 gives r0..r3 = a0..a3.
