@@ -231,8 +231,8 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
 // blocks at a time in registers, and draws its best k - 1 pairs one by one: each lane knows its best
 // remaining pair, two warp reductions find the best score and its lowest block, the owner looks for its
 // next. Rounds, and then the warps, pass on only those k - 1. (Per-lane insertion lists with a shuffle
-// merge took 31 us for 64 sequences in [16K, 128K] and 4 groups, traced; this takes 13.)
-constexpr int kTopkWarps = 4, kTopkPer = 8;
+// merge took 31 us for 64 sequences in [16K, 128K] and 4 groups, traced; this takes 10.)
+constexpr int kTopkWarps = 8, kTopkPer = 4;
 
 // Integers that order like the scores (-0 and +0 are one value), 0 for none.
 __device__ __forceinline__ uint32_t score_key(float v)
@@ -241,8 +241,8 @@ __device__ __forceinline__ uint32_t score_key(float v)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Draws the best `want` of the warp's 32 * N pairs (key, block; key 0: none) in order into the arrays held by
-// lanes 0 .. want - 1. Ties go to the lower block.
+// Draws the best `want` of the warp's 32 * N pairs (key, block; key 0: none), in order, into lanes 0 .. want - 1.
+// Ties go to the lower block; a lane's blocks ascend with i.
 template <int N>
 __device__ __forceinline__ void draw_best(uint32_t (&key)[N], int (&blk)[N], int want, uint32_t& best_key, int& best_blk)
 {
@@ -256,7 +256,7 @@ __device__ __forceinline__ void draw_best(uint32_t (&key)[N], int (&blk)[N], int
         at = 0x7FFFFFFF;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (key[i] > top || (key[i] == top && key[i] != 0u && blk[i] < at)) top = key[i], at = blk[i];
+            if (key[i] > top) top = key[i], at = blk[i];
     };
     find();
     for (int j = 0; j < want; ++j) {
@@ -297,25 +297,25 @@ __global__ void __launch_bounds__(kTopkWarps * 32) decode_topk_kernel(DecodeArgs
     const int local = seq_local_block(len), want = a.k - 1;
     const float* row = a.pooled + seg * nb_max;
     const int part = (local + kTopkWarps - 1) / kTopkWarps, b0 = min(local, warp * part), b1 = min(local, b0 + part);
-    uint32_t key[kTopkPer + 1]; // the last: what the rounds before passed on
-    int blk[kTopkPer + 1];
-    key[kTopkPer] = 0u;
-    blk[kTopkPer] = 0x7FFFFFFF;
+    uint32_t key[1 + kTopkPer]; // the first: what the rounds before passed on
+    int blk[1 + kTopkPer];
+    key[0] = 0u;
+    blk[0] = 0x7FFFFFFF;
     for (int j0 = b0; j0 < b1; j0 += 32 * kTopkPer) {
 #pragma unroll
         for (int i = 0; i < kTopkPer; ++i) {
-            blk[i] = j0 + 32 * i + lane;
-            key[i] = blk[i] < b1 ? score_key(row[blk[i]]) : 0u;
+            blk[1 + i] = j0 + 32 * i + lane;
+            key[1 + i] = blk[1 + i] < b1 ? score_key(row[blk[1 + i]]) : 0u;
         }
         uint32_t bk;
         int bb;
         draw_best(key, blk, want, bk, bb);
-        key[kTopkPer] = bk;
-        blk[kTopkPer] = bb;
+        key[0] = bk;
+        blk[0] = bb;
     }
     if (lane < kMaxK) {
-        keys[warp][lane] = key[kTopkPer];
-        blks[warp][lane] = blk[kTopkPer];
+        keys[warp][lane] = key[0];
+        blks[warp][lane] = blk[0];
     }
     __syncthreads();
     if (warp != 0) return;
