@@ -19,9 +19,9 @@
 //   O = P V: lane (g, t) holds d_h / 8 consecutive codes of four keys, so column g of output tile n is
 //     element g * d_h / 8 + n, and the nibbles of two keys are joined before the conversion.
 // q is held in fp16 as q * 2^-e with e the exponent of the row's largest |q| (elements lose bits only
-// below 2^-14 of it, an error of 2^-25 of it at most); P in fp16 relative to a reference at most 2^15
-// below its largest value (relative error 2^-12; weights below 2^-24 of fp16's unit, 2^-31 of the
-// largest, are the first to lose bits). Sums, maxima and outputs are fp32.
+// below 2^-14 of it, an error of 2^-25 of it at most); P in fp16 relative to a reference that leaves its
+// largest value in [2^7, 2^15] (off by 2^-11 of itself at most; weights below 2^-21 of the largest may be
+// subnormal and are off by 2^-32 of the largest at most). Sums, maxima and outputs are fp32.
 #include <math_constants.h>
 
 #include "kv4.cuh"

@@ -8,8 +8,12 @@ from what is rounded (half steps: bf16 2^-8, fp16 2^-11, fp32 2^-24 of the value
           and S' = max|q| sum|K| / sqrt(d) <= d S''; taken together as e = 2^-16 S + 2^-25 S'.
   lse     e + 2^-22 |lse| (stored in fp32, from a base-2 logarithm) + 2^-20 (ex2 and the sums).
   weights p (2 e + 2^-19): exp of two logit errors, ex2's 2^-22, sums of up to 16 heads.
-  out     p is rounded to fp16 (2^-11 of it at most) and sums are fp32, so before rounding the error is
-          (2^-11 + 2 e + 2^-19) sum_j p_j |V_j|; then bf16: 2^-8 |out|."""
+  out     p is rounded to fp16 (2^-11 of it at most, while it is a normal number) and sums are fp32, so before
+          rounding the error is (2^-11 + 2 e + 2^-19) sum_j p_j |V_j|; then bf16: 2^-8 |out|. P is held against a
+          reference set 7 powers of two below the row's maximum and raised, never lowered: the largest weight
+          has P >= 2^7. A P below fp16's normal range is off by half a subnormal step, 2^-25, which is at most
+          2^-25 / 2^7 = 2^-32 of the largest weight, itself at most 1: + 2^-32 sum_j |V_j|. It shows where the
+          heavy keys' V is 0, so that keys of p = 1e-9 are all that an element holds."""
 import numpy as np
 import pytest
 
@@ -75,7 +79,7 @@ def check_decode(c, q, lens, out, lse, block_idx=None, w=None, w_out=None, w_bef
             want, wl, p, pv, S = ref.attend(qh[b, hs], K, V)
             big = float((np.abs(qh[b, hs]).max(-1)[:, None] * np.abs(K).sum(-1)[None]).max() / np.sqrt(d)) if len(pos) else 0.0
             e = 2.0 ** -16 * S + 2.0 ** -25 * big
-            tol = (2.0 ** -11 + 2 * e + 2.0 ** -19) * pv + 2.0 ** -8 * np.abs(want)
+            tol = (2.0 ** -11 + 2 * e + 2.0 ** -19) * pv + 2.0 ** -8 * np.abs(want) + 2.0 ** -32 * np.abs(V).sum(0)
             assert np.isfinite(oh[b, hs]).all()
             bad = np.abs(oh[b, hs] - want) > tol + 1e-30
             assert not bad.any(), (b, r, n, np.argwhere(bad)[:3], np.abs(oh[b, hs] - want).max())
@@ -191,7 +195,7 @@ def test_decode_hard_values():
         v[100] *= 2000.0
         v[2500:2600] *= 1e-2
 
-    c = fill_cache(B, 3072 + 128, H, d, [n, n], seed=3, ts=(0.5, 1.0), v_bump=bump)
+    c = fill_cache(B, 3200, H, d, [n, n], seed=3, ts=(0.5, 1.0), v_bump=bump)
     q = torch.randn((B, H * G, d), device="cuda")
     for h, f in enumerate([0.0, 1e-30, 1e-4, 1.0, 20.0, 60.0, 3.0, 1.0]):
         q[:, h] *= f
@@ -201,6 +205,24 @@ def test_decode_hard_values():
     q = q.bfloat16()
     out, lse = msa.msa_kv4_decode(q, c, i32([n, n]))
     check_decode(c, q, [n, n], out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_light_keys(d):
+    """One key outweighs the rest by 2^29 and its V is 0 in half of the elements: those hold what the others give."""
+    B, H, G, n = 1, 1, 16, 700
+    c = make_cache(B, 768, H, d)
+    g = torch.Generator("cuda").manual_seed(17)
+    k = torch.zeros((n, H, d), device="cuda")
+    k[5, 0, 0] = 4.0
+    v = torch.randn((n, H, d), device="cuda", generator=g)
+    v[5, :, : d // 2] = 0.0
+    msa.msa_kv4_append(c, k.bfloat16(), v.bfloat16(), i32([0]), i32([0, n]))
+    q = torch.zeros((B, H * G, d), device="cuda")
+    q[:, :, 0] = 20.1 / 4.0 * d ** 0.5 * torch.linspace(0.2, 1.1, G, device="cuda")
+    q = q.bfloat16()
+    out, lse = msa.msa_kv4_decode(q, c, i32([n]))
+    check_decode(c, q, [n], out, lse)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -294,7 +316,8 @@ def test_decode_offsets_past_32_bits():
         want = p[:, :n] @ V
         got = out[-1, r].double().cpu().numpy()
         e = 2.0 ** -16 * (np.abs(qh) @ np.abs(K).T).max() / np.sqrt(d) + 2.0 ** -25 * np.abs(qh).max() * np.abs(K).sum(-1).max() / np.sqrt(d)
-        assert (np.abs(got - want[0]) <= (2.0 ** -11 + 2 * e + 2.0 ** -19) * (p[:, :n] @ np.abs(V))[0] + 2.0 ** -8 * np.abs(want[0])).all()
+        tol = (2.0 ** -11 + 2 * e + 2.0 ** -19) * (p[:, :n] @ np.abs(V))[0] + 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -32 * np.abs(V).sum(0)
+        assert (np.abs(got - want[0]) <= tol).all()
     to = msa.KV4Cache.empty(B, 2048, H, d)
     w = torch.zeros((B, H, L_max), device="cuda")
     w[-1, :, at:] = torch.rand((H, n), device="cuda") + 1
@@ -311,7 +334,7 @@ def test_sparse_decode(shape):
     """Selections equal msa_sparse_decode's on the same index keys; the attention is that of the 4-bit values."""
     H, d, G, d_idx, k = shape
     lens = [1, 128, 129, 3000, 2500, 777]
-    B, L_max = len(lens), 3072 + 128
+    B, L_max = len(lens), 3200
     c = fill_cache(B, L_max, H, d, lens, seed=11)
     g = torch.Generator("cuda").manual_seed(12)
     q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
