@@ -22,6 +22,7 @@
 // below 2^-14 of it, an error of 2^-25 of it at most); P in fp16 relative to a reference that leaves its
 // largest value in [2^7, 2^15] (off by 2^-11 of itself at most; weights below 2^-21 of the largest may be
 // subnormal and are off by 2^-32 of the largest at most). Sums, maxima and outputs are fp32.
+#include <cfloat>
 #include <math_constants.h>
 
 #include "kv4.cuh"
@@ -195,7 +196,8 @@ __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int
         // 2^e <= mx; e within [-126, 126] so that 2^-e is a normal number too
         const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        (half ? f1 : f0) = base * __uint_as_float((uint32_t)(127 + e) << 23);
+        // finite and above 0, so that it maps a sum of 0 to 0 and a masked -inf to -inf
+        (half ? f1 : f0) = fminf(fmaxf(base * __uint_as_float((uint32_t)(127 + e) << 23), FLT_MIN), FLT_MAX);
 #pragma unroll
         for (int i = 0; i < DH / 8; ++i) // pair i: elements 2 i, 2 i + 1 of the lane's run
             qf[i / 2][2 * (i & 1) + half] = pack_f16x2(bf16_lo(x[i]) * down, bf16_hi(x[i]) * down);

@@ -404,7 +404,7 @@ typedef struct {
  * position starts[b] + i - cu_seqlens[b] of sequence b (prompt chunks; empty sequences allowed).
  *   k, v       : [T, H_kv, d_h] bf16, rows k_stride / v_stride elements apart (at least H_kv * d_h, a
  *                multiple of 8: slices of a fused projection's output need no copy), 16-byte aligned
- *   starts     : [B] int32 device;  cu_seqlens : [B + 1] int32 device, or NULL;  T >= 0
+ *   starts     : [B] int32 device;  cu_seqlens : [B + 1] int32 device, or NULL;  0 <= T <= B * L_max
  * Rows that the tables put outside the cache or outside [cu_seqlens[0], cu_seqlens[B]) are left out
  * and reported (MSA_ERR_DEVICE_CHECK). No other row of the cache changes.
  *

@@ -207,6 +207,23 @@ def test_decode_hard_values():
     check_decode(c, q, [n, n], out, lse)
 
 
+@pytest.mark.parametrize("G", [3, 16])
+@pytest.mark.parametrize("scale, zero", [(2.0 ** -40, "q"), (2.0 ** -100, "q"), (2.0 ** 10, "K")])
+def test_decode_factor_range(scale, zero, G):
+    """Zero q rows (a padded batch) on a cache of tiny values, and enormous q on zero keys: all logits are 0, the
+    factor on them leaves fp32's range, and the last tile is masked. Every visible key weighs the same."""
+    B, H, d, n = 1, 2, 128, 45
+    c = make_cache(B, 128, H, d, (scale, 1.0))
+    g = torch.Generator("cuda").manual_seed(23)
+    k = torch.randn((n, H, d), device="cuda", generator=g) * (scale if zero == "q" else 0.0)
+    v = torch.randn((n, H, d), device="cuda", generator=g)
+    msa.msa_kv4_append(c, k.bfloat16(), v.bfloat16(), i32([0]), i32([0, n]))
+    q = torch.full((B, H * G, d), 0.0 if zero == "q" else 2.0 ** 125, device="cuda").bfloat16()
+    w_out = torch.zeros((B, H, 128), device="cuda")
+    out, lse = msa.msa_kv4_decode(q, c, i32([n]), weights_out=w_out)
+    check_decode(c, q, [n], out, lse, w_out=w_out, w_before=torch.zeros_like(w_out))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_light_keys(d):
     """One key outweighs the rest by 2^29 and its V is 0 in half of the elements: those hold what the others give."""
@@ -378,6 +395,31 @@ def test_sparse_selection_long(k):
         want[:len(best) + 1] = np.sort(np.append(best, local))
         assert sel[b, 0].tolist() == want.tolist(), b
     check_decode(c, q, lens, out, lse, sel.cpu().numpy(), None, w_out, torch.full_like(w_out, 4.0))
+
+
+@pytest.mark.parametrize("k", [3, 4, 16])
+def test_sparse_selection_infinite_scores(k):
+    """Blocks whose scores are all -inf come last, the lower first, and still fill a selection that has room; the
+    cache in bf16 selects the same."""
+    B, H, G, d, d_idx, n = 1, 1, 4, 64, 32, 700
+    c = fill_cache(B, 768, H, d, [n], seed=51)
+    g = torch.Generator("cuda").manual_seed(52)
+    q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
+    q_idx = torch.full((B, H, d_idx), 2.0 ** 100, device="cuda").bfloat16()
+    k_idx = torch.full((B, 768, H, d_idx), -1.0, device="cuda").bfloat16()
+    k_idx[:, :128] = k_idx[:, 384:512] = -2.0 ** 100     # products of -2^200: blocks 0 and 3
+    k_idx[:, 256:384] = 1.0                              # block 2 is the best
+    want = {3: [1, 2, 5], 4: [1, 2, 4, 5], 16: [0, 1, 2, 3, 4, 5] + [-1] * 10}[k]
+    out, lse, sel = msa.msa_sparse_decode_kv4(q, q_idx, c, k_idx, i32([n]), 128, k)
+    assert sel.flatten().tolist() == want
+    check_decode(c, q, [n], out, lse, sel.cpu().numpy())
+    cu = i32([0, 768])
+    c.k_scales[:, :, n:], c.v_scales[:, :, n:] = 0, 0
+    kb, vb = msa.msa_kv4_read(c, i32([0]), cu, 768)
+    o2, _, s2 = msa.msa_sparse_decode(q, q_idx, kb[None], vb[None], k_idx, i32([n]), 128, k)
+    assert torch.equal(s2, sel)
+    # bf16 P (twice 2^-8: above and below the line), partial and outputs: below 6 half steps of the largest |V|
+    assert (o2.float() - out.float()).abs().max() <= 6 * 2.0 ** -8 * vb.float().abs().max()
 
 
 # ------------------------------------------------------------------------------------------ eviction
