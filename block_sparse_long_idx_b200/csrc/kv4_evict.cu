@@ -38,13 +38,33 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 struct SelShared {
     // digits alternate between two histograms, so that one barrier each is enough (and two CTAs fit an SM)
     int hist[2][kBins * kCopies];
-    int sums[2][kBins]; // of the CTA's copies, read by the cluster
-    int tmp[kSelWarps];
+    int sums[2][kBins], coarse[2][kBins / 32]; // of the CTA's copies, and of 32 bins each, read by the cluster
     uint32_t prefix; // of the key looked for, and how many of its equals are still to be taken
     int need, whole;
     int ties[kSelWarps], takes[kSelWarps];
     int cta_ties, cta_sure; // this CTA's equal keys, and tokens kept without a choice
 };
+
+// f(r) for every CTA r of the cluster, its loads in flight together.
+template <class F>
+__device__ __forceinline__ void for_ranks(int size, F f)
+{
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < size) f(r);
+}
+
+// The sum of x over this lane and the lower ones.
+__device__ __forceinline__ int warp_sum_upto(int x)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
 
 // Every warp owns a contiguous run of tokens, walked in rounds of 32 * KEYS. RESIDENT: the run is one round,
 // whose keys are read from memory once and stay in registers.
@@ -108,45 +128,41 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictArgs a)
                         atomicAdd(&sh.hist[d & 1][((key[i] >> shift) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
             }
             __syncthreads();
-            int* sums = sh.sums[d & 1];
-            for (int i = tid; i < kBins; i += kSelThreads) {
+            int *sums = sh.sums[d & 1], *coarse = sh.coarse[d & 1];
+#pragma unroll
+            for (int u = 0; u < kBins / kSelThreads; ++u) { // a warp sums 32 neighbouring bins
+                const int i = u * kSelThreads + tid;
                 const int4 h = *reinterpret_cast<const int4*>(&sh.hist[d & 1][i * kCopies]);
-                sums[i] = h.x + h.y + h.z + h.w;
+                const int x = h.x + h.y + h.z + h.w;
+                sums[i] = x;
+                const int all = __reduce_add_sync(0xffffffffu, x);
+                if (lane == 0) coarse[i / 32] = all;
             }
             cluster.sync();
-            // bins in descending order, four to a thread: the one where the counts reach `need`
-            constexpr int PER = kBins / kSelThreads;
-            static_assert(PER == 4, "a thread's bins are one 16-byte read");
-            const int top = kBins - PER * (tid + 1); // bins top + 3 .. top
-            int4 x = make_int4(0, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) { // loads in flight together
-                if (r < size) {
-                    const int4 y = *reinterpret_cast<const int4*>(cluster.map_shared_rank(sums, r) + top);
-                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                }
-            }
-            const int mine = x.x + x.y + x.z + x.w;
-            int incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (lane == 31) sh.tmp[warp] = incl;
-            __syncthreads();
-            int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sh.tmp[lane] : 0);
-            const int count[PER] = {x.w, x.z, x.y, x.x};
-#pragma unroll
-            for (int u = 0; u < PER; ++u) {
-                if (before < need && before + count[u] >= need) { // one bin of one thread
-                    const uint32_t prefix = T | ((uint32_t)(top + PER - 1 - u) << shift);
+            // in descending order, the 32 bins in which the counts reach `need`, and then the bin
+            if (warp == 0) {
+                static_assert(kBins == 64 * 32, "two groups of bins to a lane");
+                int2 c = make_int2(0, 0); // groups 62 - 2 lane and the one above it
+                for_ranks(size, [&](int r) {
+                    const int2 y = reinterpret_cast<const int2*>(cluster.map_shared_rank(coarse, r))[31 - lane];
+                    c.x += y.x, c.y += y.y;
+                });
+                const int upto = warp_sum_upto(c.x + c.y), above2 = upto - c.x - c.y;
+                const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= need)) - 1; // candidates are `need` or more
+                const bool second = above2 + c.y < need;
+                const int group = __shfl_sync(0xffffffffu, 62 - 2 * lane + !second, owner);
+                const int before = __shfl_sync(0xffffffffu, above2 + (second ? c.y : 0), owner);
+                const int bin = 32 * group + 31 - lane;
+                int x = 0;
+                for_ranks(size, [&](int r) { x += cluster.map_shared_rank(sums, r)[bin]; });
+                const int reach = before + warp_sum_upto(x);
+                if (reach >= need && reach - x < need) { // one lane
+                    const uint32_t prefix = T | ((uint32_t)bin << shift);
                     // a bin that is taken whole: its keys are those above prefix - 1, and no further digit is needed
-                    sh.whole = before + count[u] == need && prefix != 0u;
+                    sh.whole = reach == need && prefix != 0u;
                     sh.prefix = sh.whole ? prefix - 1u : prefix;
-                    sh.need = sh.whole ? 0 : need - before;
+                    sh.need = sh.whole ? 0 : need - (reach - x);
                 }
-                before += count[u];
             }
             __syncthreads();
             T = sh.prefix;
