@@ -291,8 +291,9 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4EvictArgs a)
 
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s)
 {
-    // keys in registers where a cluster of up to 8 CTAs holds a full cache (16 keys to a thread, 32 above
-    // 65536 tokens); longer caches are read again for every digit
+    // keys in registers where a cluster of up to 8 CTAs holds a full cache (16 keys to a thread, 32 above 65536
+    // tokens): 16 prompts in caches of 32768, cut to 4096 and read back, take 91 us so, 94 with 32 keys to a
+    // thread of half the CTAs, 156 with keys read again for every digit, as longer caches need
     constexpr int kCta = kSelThreads * 16;
     int size = 1;
     while (size < kMaxCluster && (int64_t)size * kCta < a.L_max) size *= 2;
