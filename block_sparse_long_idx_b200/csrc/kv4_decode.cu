@@ -165,6 +165,7 @@ struct Shared {
     uint64_t full[kStages], empty[kStages];
     float m[kSlots][16], l[kSlots][16];
     uint4 q[8][32]; // Q fragments of the segment
+    float2 f[32];   // the lanes' factors on its sums (load_q)
     int warp_units[kLaunch / 32];
     int b0, seg0; // sequence holding the slice's first unit, first unit of that sequence
     int abort_flag;
@@ -334,6 +335,10 @@ __device__ __forceinline__ void finish(const Kv4DecodeArgs& a, int64_t row, int 
 // The consumers' barrier (the producer's warpgroup takes no part).
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
+// A second one, at which half of the warps only arrive: the join scratch is free again.
+__device__ __forceinline__ void scratch_release() { asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void scratch_acquire() { asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory"); }
+
 template <int DH, bool GIVEN, bool NARROW>
 __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
 {
@@ -452,17 +457,25 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
         __syncwarp(); // every lane has read the stage
         if (lane == 0) mbar_arrive(&sh.empty[st]);
     };
-    uint32_t used = 0; // chunks
-    bool ok = true;
-    for (; cons.more(); cons.next_segment(w)) {
-        if (cons.pos >= cons.end) continue;
+    // one warp loads a segment's q, for the second and later ones while the segment before is joined
+    auto fetch_q = [&](int b, int r) {
         float f0, f1;
-        {
-            uint32_t qf[DH / 16][4];
-            load_q<DH, NARROW>(a, cons.b, cons.r, G, g, t, qf, f0, f1);
-            if (warp == 0) store_q<DH, NARROW>(sh.q, qf, lane);
-        }
-        sync_consumers();
+        uint32_t qf[DH / 16][4];
+        load_q<DH, NARROW>(a, b, r, G, g, t, qf, f0, f1);
+        store_q<DH, NARROW>(sh.q, qf, lane);
+        sh.f[lane] = make_float2(f0, f1);
+    };
+    auto to_work = [&](Walk<GIVEN>& x) { // on to a segment with blocks in the slice
+        while (x.more() && x.pos >= x.end) x.next_segment(w);
+    };
+    to_work(cons);
+    if (warp == kWarps - 1 && cons.more()) fetch_q(cons.b, cons.r);
+    sync_consumers();
+    uint32_t used = 0; // chunks
+    bool ok = true, first = true;
+    for (; cons.more(); cons.next_segment(w), to_work(cons), first = false) {
+        if (!first && warp < kSlots) scratch_release();
+        const float f0 = sh.f[lane].x, f1 = sh.f[lane].y;
         // outputs: o[n][2 h + c], of head g + 8 h and element (2 t + c) NT + n; NARROW: o[i][2 u + h], of head 2 t + h
         // and element g NT + 2 i + u
         float o[NARROW ? NT / 2 : NT][4];
@@ -649,8 +662,17 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 for (int e = 0; e < RUN; e += 4)
                     *reinterpret_cast<float4*>(mine + (h ? h1 : h0) * C::ROW + e) = make_float4(at(h, e), at(h, e + 1), at(h, e + 2), at(h, e + 3));
         };
-        if (warp >= kSlots) put();
+        if (warp >= kSlots) {
+            if (!first) scratch_acquire();
+            put();
+        }
         sync_consumers();
+        if (warp == kWarps - 1) {
+            Walk<GIVEN> next = cons;
+            next.next_segment(w);
+            to_work(next);
+            if (next.more()) fetch_q(next.b, next.r);
+        }
         if (warp < kSlots) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -702,7 +724,6 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 }
             }
         }
-        sync_consumers(); // the join scratch is free again
     }
 }
 
