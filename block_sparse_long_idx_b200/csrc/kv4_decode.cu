@@ -39,11 +39,11 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kLaunch = kThreads + 128; // and one warpgroup whose first thread starts the copies
 constexpr int kRegs = 160, kProducerRegs = 32; // of the 128 a thread is launched with
 static_assert(kThreads * kRegs + 128 * kProducerRegs <= kLaunch * 128, "register split");
-// What joining a segment costs, in blocks: it counts in the split of the work. Measured with 3, 4, 6 and 8:
-// 24 ragged sequences of 8 heads of 64 take 31.9, 31.0, 28.6 and 28.1 us, one sequence with 16 given blocks
-// 18.2, 18.2, 19.9 and 21.9 us (fewer CTAs then).
+// What joining a segment costs, in blocks: it counts in the split of the work. Graph replays: 24 ragged
+// sequences of 8 heads of 64 take 26.5, 25.5 and 25.4 us with 4, 5 and 6; the block-sparse decode of one
+// sequence (16 blocks given) 30.1, 30.2 and 30.8 us with 2, 3 and 4, of 64 sequences 393 to 395 with any.
 template <bool GIVEN>
-constexpr int kJoin = GIVEN ? 4 : 6;
+constexpr int kJoin = GIVEN ? 3 : 6;
 constexpr int kSlots = kWarps / 2; // join scratch: one output per pair of warps
 constexpr int kTile = 32;          // keys of a warp's part
 constexpr float kHeadroom = 7.f;   // P's reference: log2 units below the maximum it was set from
