@@ -595,6 +595,11 @@ def _kv4_decode_bytes(B, H_q):
     return lib.msa_kv4_decode_workspace_size(B, H_q)
 
 
+@functools.lru_cache
+def _sparse_decode_kv4_bytes(B, L_max, H_q, H_kv, B_k, k):
+    return lib.msa_sparse_decode_kv4_workspace_size(B, L_max, H_q, H_kv, B_k, k)
+
+
 @_on_device
 def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weights_out=None, decay: float = 1.0, out=None,
                    lse=None, want_lse: bool = True, workspace=None, stream=None):
@@ -638,11 +643,10 @@ def msa_sparse_decode_kv4(q, q_idx, cache: KV4Cache, k_idx_cache, lens, B_k: int
     if out is None:
         out = torch.empty_like(q)
     if lse is None and want_lse:
-        lse = torch.empty((cache.B, H_q), dtype=torch.float32, device=cache.device)
+        lse = torch.empty_strided((cache.B, H_q), (H_q, 1), dtype=torch.float32, device=cache.device)
     if block_idx_out is None:
         block_idx_out = torch.empty((cache.B, cache.H_kv, max(k, 0)), dtype=torch.int32, device=cache.device)
-    ws = _workspace(lib.msa_sparse_decode_kv4_workspace_size(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k), cache.device,
-                    workspace)
+    ws = _workspace(_sparse_decode_kv4_bytes(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k), cache.device, workspace)
     _check("msa_sparse_decode_kv4", lib.msa_sparse_decode_kv4(
         cache._ref, q.data_ptr(), q_idx.data_ptr(), k_idx_cache.data_ptr(), lens.data_ptr(), H_q, d_idx, B_k, k,
         _ptr(weights), _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), block_idx_out.data_ptr(), ws.data_ptr(),
@@ -681,7 +685,8 @@ def msa_kv4_evict(cache: KV4Cache, to: KV4Cache, weights, lens, keep: int, recen
     if lens_out is None:
         lens_out = torch.empty_like(lens)
     if kept is None:
-        kept = torch.empty((cache.B, cache.H_kv, max(keep, 0)), dtype=torch.int32, device=dev)
+        keep_ = max(keep, 0)
+        kept = torch.empty_strided((cache.B, cache.H_kv, keep_), (cache.H_kv * keep_, keep_, 1), dtype=torch.int32, device=dev)
     ws = None if workspace is None else _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
     _check("msa_kv4_evict", lib.msa_kv4_evict(
         cache._ref, to._ref, weights.data_ptr(), lens.data_ptr(), keep, recent, first, _ptr(k_idx_cache), _ptr(k_idx_dst),
