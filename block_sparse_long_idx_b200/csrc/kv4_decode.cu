@@ -823,7 +823,8 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         before += n;
     }
     __syncthreads();
-    pdl_wait(); // for the lse
+    bool waited = GIVEN; // for the lse; for the blocks too, at once
+    if (GIVEN) pdl_wait();
     const bool rest = !(a.w_in == a.w_out && a.decay == 1.f); // keys of other blocks change too
     Walk<false> cons;
     for (cons.begin(w, b0, seg0, lo, hi); cons.more(); cons.next_segment(w)) {
@@ -836,10 +837,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
             if (warp == 0) store_q<DH, NARROW>(q, qf, lane);
         }
         __syncthreads();
-        const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
-        const int h0 = NARROW ? 2 * t : g, h1 = NARROW ? 2 * t + 1 : g + 8;
-        const float z0 = h0 < G ? lse[h0] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
-        const float z1 = h1 < G ? lse[h1] * 1.4426950408889634f : CUDART_INF_F;
+        float z0, z1;
         int mine = -1; // given blocks: the first key of this lane's
         if (GIVEN && lane < a.k) mine = Work<true>{a}.key0(cons.b, cons.r, lane, cons.len);
         const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
@@ -892,7 +890,16 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
             if (now.key0 + my_key < last) a.w_out[row0 + now.key0 + my_key] = now.old + add;
         };
         Tile even, odd;
-        for (fetch(even); even.key0 < last;) {
+        fetch(even);
+        if (!waited) { // q and the first keys are on their way
+            pdl_wait();
+            waited = true;
+        }
+        const float* lse = a.lse + (int64_t)cons.b * a.H_q + cons.r * G;
+        const int h0 = NARROW ? 2 * t : g, h1 = NARROW ? 2 * t + 1 : g + 8;
+        z0 = h0 < G ? lse[h0] * 1.4426950408889634f : CUDART_INF_F; // rows past the heads weigh nothing
+        z1 = h1 < G ? lse[h1] * 1.4426950408889634f : CUDART_INF_F;
+        while (even.key0 < last) {
             fetch(odd);
             finish_tile(even);
             if (odd.key0 >= last) break;
@@ -900,6 +907,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
             finish_tile(odd);
         }
     }
+    if (!waited) pdl_wait(); // a slice without blocks
 }
 
 template <int DH, bool GIVEN, bool NARROW>
