@@ -4,7 +4,10 @@
 //   x_j = q[h] . K[j] / sqrt(d_h),  out[h] = sum_j softmax(x)_j V[j],  lse[h] = log sum_j exp(x_j)
 //   w_out[r][j] = decay * w_in[r][j] + sum over the heads of r of softmax(x)_j      (optional)
 //
-// Bound by reading the cache (d_h + d_h / 8 bytes per token and KV head). One CTA per SM walks an
+// It has to read the cache (d_h + d_h / 8 bytes per token and KV head); with 16 heads of 128 the conversions and
+// MMAs of a key, whose issue adds up (6.5 clocks per SM and 8 codes a lane), take longer: 32 sequences in
+// [16K, 128K] with 64 heads on 4 take 300 us, 4.5 TB/s of the 6.5 that a copy moves; with up to 8 heads a
+// KV head 16 sequences in [8K, 16K] with 8 KV heads take 51 us, of which 35 are the copy's. One CTA per SM walks an
 // equal contiguous slice of the flattened list of 128-key blocks of all (sequence, KV head) pairs, so
 // ragged batches and single long sequences load every SM alike. Bulk copies bring kBlocks blocks at a
 // time into a ring of kStages such chunks; every warp takes 32 keys of a chunk and keeps a running
@@ -729,7 +732,8 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
 
 // Joins the partials of the segments that several CTAs share. CTA (c, y): the segment whose first block is in
 // CTA c's slice and whose last is not (there is at most one), heads kJoinRows y and on; kJoinGroups warps a
-// head, each with every kJoinGroups-th partial, in a fixed order.
+// head, each with every kJoinGroups-th partial, in a fixed order. Bound by latency (37 partials of 16 heads for each
+// KV head of one long sequence): it starts early, and finds its segment before it waits for the attention.
 constexpr int kJoinRows = 4, kJoinGroups = 4, kJoinThreads = kJoinRows * kJoinGroups * 32;
 
 template <int DH, bool GIVEN>
@@ -795,7 +799,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeArgs a)
 
 // Accumulated weights, after the attention (they need the final lse): K is read once more. A warp takes 32
 // visible keys at a time and writes decay * w_in plus the group's sum of softmax weights; with given blocks
-// the keys of the others get decay * w_in alone.
+// the keys of the others get decay * w_in alone. 16 sequences in [1K, 16K] with 64 heads on 4: 21 us, of which
+// reading K, w_in and writing w_out are 7; conversions, MMAs and the latency of short slices are the rest.
 constexpr int kWThreads = 256;
 
 template <int DH, bool GIVEN, bool NARROW>
@@ -941,8 +946,8 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t s)
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s)
 {
     // up to 8 heads a KV head: keys are the rows of the products and heads the 8 columns, half the tensor-core
-    // work of 16 rows that are mostly padding. 16 sequences in [8K, 16K] of 8 KV heads of 128 take 50 us with 1
-    // head each, 51 with 8 and 68 with 16; with 16 rows for all 61, 63 and 68.
+    // work of 16 rows that are mostly padding. 16 sequences in [8K, 16K] of 8 KV heads of 128 take 51 us with 1
+    // head each, 51 with 8 and 67 with 16; with 16 rows for all 61, 63 and 68.
     const bool narrow = a.H_q / a.H_kv <= 8, given = a.block_idx != nullptr;
     if (a.d_h == 128) {
         if (given) return narrow ? launch<128, true, true>(a, s) : launch<128, true, false>(a, s);

@@ -9,7 +9,10 @@
 //            integers, most significant first, histograms in shared memory summed over the cluster),
 //            then writes the kept positions in order: every warp counts in a contiguous run, the counts
 //            are scanned over warps and CTAs, and a second walk writes. No atomics decide an order.
-//   move   : CTAs of 64 kept rows; a thread starts all its loads before its stores.
+//            Bound by the latency of its rounds: 16 sequences in [20K, 32K] take 21 us, where reading the
+//            weights takes 1.
+//   move   : CTAs of 64 kept rows; a thread starts all its loads before its stores. Bound by memory: 4096 rows of
+//            each, with index keys of 64, take 28 us (5.6 TB/s; kept rows lie 72 and 128 bytes at a time).
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
