@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeArgs a)
     __shared__ float4 sv[kJoinRows][kJoinGroups][L4];
     __shared__ float2 sml[kJoinRows][kJoinGroups];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_trigger();
+    if (a.w_out) pdl_trigger(); // for the weights; else the call ends here
     const Work<GIVEN> w{a};
     int before, b_lo, b_hi;
     const int total = total_units<kJoinThreads>(w, warp_units, before, b_lo, b_hi);
