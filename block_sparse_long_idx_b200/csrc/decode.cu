@@ -32,6 +32,9 @@ constexpr int kPoolStageBytes = kBk * 512;         // one block of rows up to 51
 
 struct PoolShared {
     uint64_t full[kPoolStages], empty[kPoolStages];
+    int64_t warp_blocks[kPoolConsumers + 1];
+    int64_t first; // first block, in the list, of the sequence the slice begins in
+    int beta;      // that sequence
     float pmax[kPoolStages][kPoolConsumers][32]; // [stage][warp][group]: the warp's rows' maximum
     int abort_flag;
 };
@@ -40,51 +43,11 @@ constexpr int kPoolSmem = kPoolStages * kPoolStageBytes + (int)sizeof(PoolShared
 __device__ __forceinline__ int seq_local_block(int len) { return (len - 1) / kBk; }
 
 // ----------------------------------------------------------------------------------- 1. pooling
-// Work balance: sequences have very different lengths, so the fully visible blocks of all
-// sequences form one flattened list (prefix[beta] = blocks of the sequences before beta) and every
-// warp of a persistent grid streams an equal contiguous slice of it.
-__global__ void __launch_bounds__(1024) decode_prefix_kernel(DecodeArgs a)
-{
-    __shared__ int64_t warp_sum[32];
-    __shared__ int64_t carry;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_trigger();
-    if (tid == 0) {
-        carry = 0;
-        a.blk_prefix[0] = 0;
-    }
-    __syncthreads();
-    for (int base = 0; base < a.B; base += 1024) {
-        const int beta = base + tid;
-        int64_t n = 0;
-        if (beta < a.B) {
-            const int len = a.lens[beta];
-            n = (len >= 1 && len <= a.L_max) ? seq_local_block(len) : 0;
-        }
-        int64_t x = n; // inclusive scan: warp, then across warps
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sum[warp] = x;
-        __syncthreads();
-        if (warp == 0) {
-            int64_t w = warp_sum[lane];
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-                if (lane >= o) w += y;
-            }
-            warp_sum[lane] = w;
-        }
-        __syncthreads();
-        const int64_t incl = carry + x + (warp > 0 ? warp_sum[warp - 1] : 0);
-        if (beta < a.B) a.blk_prefix[beta + 1] = incl;
-        __syncthreads();
-        if (tid == 1023) carry = incl;
-        __syncthreads();
-    }
-}
-
+// Work balance: sequences have very different lengths, so the fully visible blocks of all sequences
+// form one flattened list and every CTA of a persistent grid streams an equal contiguous slice of it,
+// which it finds by summing the lengths itself (a separate kernel for their prefix cost 1.3 us more in
+// calls in a row, its launch).
+//
 // One CTA per SM streams an equal contiguous slice of the flattened block list. Its producer thread
 // keeps kPoolStages whole blocks of the k_idx cache in flight (one bulk copy each: a block's 128 rows
 // are contiguous), and kPoolConsumers warps score 128 / kPoolConsumers rows of every block from
@@ -107,18 +70,43 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
         sh.abort_flag = 0;
         fence_mbar_init();
     }
+    // every thread counts the blocks of some neighbouring sequences
+    constexpr int kThreads = (kPoolConsumers + 1) * 32;
+    auto blocks = [&](int beta) {
+        const int len = a.lens[beta];
+        return len >= 1 && len <= a.L_max ? seq_local_block(len) : 0;
+    };
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int s0 = min(a.B, (int)threadIdx.x * per), s1 = min(a.B, s0 + per);
+    int64_t mine = 0;
+    for (int beta = s0; beta < s1; ++beta) mine += blocks(beta);
+    int64_t before = mine; // inclusive over the warp, then exclusive over the CTA
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) sh.warp_blocks[warp] = before;
     __syncthreads();
-    pdl_wait(); // for the block prefix
-    const int64_t total = a.blk_prefix[a.B];
+    int64_t total = 0;
+    before -= mine;
+    for (int w = 0; w <= kPoolConsumers; ++w) {
+        if (w < warp) before += sh.warp_blocks[w];
+        total += sh.warp_blocks[w];
+    }
     const int64_t g0 = total * blockIdx.x / gridDim.x, g1 = total * (blockIdx.x + 1) / gridDim.x;
     if (g0 >= g1) return;
     volatile int* abort_flag = &sh.abort_flag;
-    // the sequence holding block g0: the last beta with prefix[beta] <= g0
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.blk_prefix[mid] <= g0) lo = mid; else hi = mid - 1;
+    for (int beta = s0; beta < s1; ++beta) { // the sequence holding block g0
+        const int n = blocks(beta);
+        if (g0 >= before && g0 < before + n) {
+            sh.beta = beta;
+            sh.first = before;
+        }
+        before += n;
     }
+    __syncthreads();
+    int beta = sh.beta;
+    int64_t first = sh.first, end = first + blocks(beta); // of sequence beta, in the list
     if (warp == kPoolConsumers) {
         // ---------------------------------------------------------------- producer (lane 0)
         if (lane != 0) return;
@@ -131,7 +119,6 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
                 a.pooled[((int64_t)pend_beta[s] * a.H_kv + r) * nb_max + pend_b[s]] = m;
             }
         };
-        int beta = lo;
         bool ok = true;
         int64_t n = 0;
         for (int64_t g = g0; g < g1; ++g, ++n) {
@@ -144,8 +131,11 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
                 }
                 flush(s);
             }
-            while (a.blk_prefix[beta + 1] <= g) ++beta;
-            const int b = (int)(g - a.blk_prefix[beta]);
+            while (end <= g) {
+                first = end;
+                end += blocks(++beta);
+            }
+            const int b = (int)(g - first);
             pend_beta[s] = beta;
             pend_b[s] = b;
             mbar_arrive_expect_tx(&sh.full[s], blk_bytes);
@@ -172,14 +162,14 @@ __global__ void __launch_bounds__((kPoolConsumers + 1) * 32, 1) decode_pool_kern
     const int r = sub / lanes_per_group;
     const int pos_lane = lane / lanes_per_pos;
     constexpr int kRows = kBk / kPoolConsumers; // rows of every block this warp scores
-    int beta = lo - 1;
+    bool entered = false;
     float qf[8];
     int64_t n = 0;
     for (int64_t g = g0; g < g1; ++g, ++n) {
         const int s = (int)(n % kPoolStages);
-        if (beta < lo || a.blk_prefix[beta + 1] <= g) { // entering the next sequence that owns blocks
-            beta = beta < lo ? lo : beta + 1;
-            while (a.blk_prefix[beta + 1] <= g) ++beta;
+        if (!entered || end <= g) { // entering the next sequence that owns blocks
+            entered = true;
+            while (end <= g) end += blocks(++beta);
             const uint4 qv = *reinterpret_cast<const uint4*>(a.q_idx + ((int64_t)beta * a.H_kv) * a.d_idx + sub * 8);
             const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
@@ -556,16 +546,14 @@ cudaError_t launch_decode_index(const DecodeArgs& a, cudaStream_t s)
     cudaError_t e0 = cudaFuncSetAttribute(decode_pool_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPoolSmem);
     if (e0 != cudaSuccess) return e0;
     trace_begin(s);
-    decode_prefix_kernel<<<1, 1024, 0, s>>>(a);
     // one CTA per SM, each an equal slice of the flattened block list
-    e0 = launch_pdl(decode_pool_kernel, dim3(n_sm), (kPoolConsumers + 1) * 32, kPoolSmem, s, a, nb_max);
-    if (e0 != cudaSuccess) return e0;
+    decode_pool_kernel<<<n_sm, (kPoolConsumers + 1) * 32, kPoolSmem, s>>>(a, nb_max);
     trace_end(s, MSA_KERNEL_DEC_POOL);
     trace_begin(s);
     e0 = launch_pdl(decode_topk_kernel, dim3(a.B, a.H_kv), kTopkWarps * 32, 0, s, a, nb_max);
     if (e0 != cudaSuccess) return e0;
     trace_end(s, MSA_KERNEL_DEC_TOPK);
-    note_launch(3);
+    note_launch(2);
     return cudaGetLastError();
 }
 

@@ -954,7 +954,6 @@ size_t msa_sparse_decode_workspace_size(int B, int64_t L_max, int H_q, int H_kv,
     sz += align_up((size_t)B * 4, 256);
     sz += align_up((size_t)B * k * H_q * d_h * 2, 256);
     sz += align_up((size_t)B * k * H_q * 4, 256);
-    sz += align_up((size_t)(B + 1) * 8, 256);
     return sz;
 }
 
@@ -1009,8 +1008,6 @@ msa_status msa_sparse_decode(const msa_bf16* q, const msa_bf16* q_idx, const msa
     a.o_part = (uint16_t*)(ws + off);
     off += align_up((size_t)B * k * H_q * d_h * 2, 256);
     a.lse_part = (float*)(ws + off);
-    off += align_up((size_t)B * k * H_q * 4, 256);
-    a.blk_prefix = (int64_t*)(ws + off);
     a.out = out;
     a.lse = lse;
     a.block_idx_out = block_idx_out;
@@ -1197,7 +1194,7 @@ size_t msa_sparse_decode_kv4_workspace_size(int B, int64_t L_max, int H_q, int H
     if (B < 1 || L_max < 1 || H_q < 1 || H_kv < 1 || B_k < 1 || k < 1) return 0;
     const int64_t nb_max = (L_max + B_k - 1) / B_k;
     return msa_kv4_decode_workspace_size(B, H_q) + align_up((size_t)B * H_kv * nb_max * 4, 256) +
-           align_up((size_t)B * H_kv * k * 4, 256) + align_up((size_t)B * 4, 256) + align_up((size_t)(B + 1) * 8, 256);
+           align_up((size_t)B * H_kv * k * 4, 256) + align_up((size_t)B * 4, 256);
 }
 
 msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_bf16* q, const msa_bf16* q_idx,
@@ -1236,8 +1233,6 @@ msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_bf16* q, 
     a.sel = (int32_t*)(ws + off);
     off += align_up((size_t)B * H_kv * k * 4, 256);
     a.nsel = (int32_t*)(ws + off);
-    off += align_up((size_t)B * 4, 256);
-    a.blk_prefix = (int64_t*)(ws + off);
     a.block_idx_out = block_idx_out;
     a.err = (int*)workspace;
     if (msa_status st = cuda_status(launch_decode_index(a, s), "decode index launch")) return st;

@@ -397,6 +397,30 @@ def test_sparse_selection_long(k):
     check_decode(c, q, lens, out, lse, sel.cpu().numpy(), None, w_out, torch.full_like(w_out, 4.0))
 
 
+def test_sparse_many_sequences():
+    """More sequences than a CTA has threads, of which many own no whole block, a run of them in a row: every
+    sequence's blocks are scored, and its outputs are those of the blocks."""
+    B, H, G, d, d_idx, k, L_max = 700, 1, 2, 64, 32, 3, 896
+    rng = np.random.default_rng(60)
+    lens = rng.integers(1, L_max + 1, size=B)
+    lens[rng.random(B) < 0.3] = 77
+    lens[100:420] = rng.integers(1, 129, size=320)
+    c = fill_cache(B, L_max, H, d, lens, seed=61)
+    g = torch.Generator("cuda").manual_seed(62)
+    q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
+    q_idx = torch.randint(-3, 4, (B, H, d_idx), device="cuda", generator=g).bfloat16()
+    k_idx = torch.randint(-3, 4, (B, L_max, H, d_idx), device="cuda", generator=g).bfloat16()
+    out, lse, sel = msa.msa_sparse_decode_kv4(q, q_idx, c, k_idx, i32(lens), 128, k)
+    s = torch.einsum("blhe,bhe->bl", k_idx.double(), q_idx.double()).view(B, L_max // 128, 128).amax(-1).cpu().numpy()
+    for b, n in enumerate(lens):
+        local = (n - 1) // 128
+        best = np.lexsort((np.arange(local), -s[b, :local]))[:k - 1]
+        want = np.full(k, -1)
+        want[:len(best) + 1] = np.sort(np.append(best, local))
+        assert sel[b, 0].tolist() == want.tolist(), b
+    check_decode(c, q, lens, out, lse, sel.cpu().numpy())
+
+
 @pytest.mark.parametrize("k", [3, 4, 16])
 def test_sparse_selection_infinite_scores(k):
     """Blocks whose scores are all -inf come last, the lower first, and still fill a selection that has room; the
