@@ -261,7 +261,7 @@ __global__ void kv2q_items_kernel(Kv2qArgs a, const int32_t* item_bases, const i
         const int32_t c = a.counts[rbw];
         const int32_t base_entry = a.bases[rbw];
         int32_t it = item_bases[x];
-        if (r == 0 && b == 0) a.window_items[w] = it;
+        if (r == 0 && b == 0) a.window_items[w] = (int32_t)min((int64_t)it, a.max_items);
         for (int32_t j = 0; j * a.chunk < c; ++j, ++it) {
             if (it >= a.max_items) {
                 report_error(a.err, MSA_ERR_DEVICE_CHECK, 101);
@@ -275,7 +275,8 @@ __global__ void kv2q_items_kernel(Kv2qArgs a, const int32_t* item_bases, const i
             a.items[it] = item;
         }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.window_items[a.n_windows] = *n_items_total;
+    // never more than the list holds, whatever the selections
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.window_items[a.n_windows] = (int32_t)min((int64_t)*n_items_total, a.max_items);
 }
 
 } // namespace

@@ -230,10 +230,30 @@ msa_status msa_index_topk(const msa_bf16* q_idx, const msa_bf16* k_idx, int64_t 
 // ------------------------------------------------------------------------------------ kv2q
 } // extern "C"
 
+// Query and key row offsets of a packed batch (host arrays, [B + 1]).
+struct PackedRows {
+    const int32_t *cu, *cu_k;
+    int B;
+};
+
+// The blocks that rows [lo, hi) of a packed batch can see: of every sequence with rows there, those up to its last one.
+// `s` (0 at first) follows the windows upwards.
+static int64_t packed_visible_blocks(const PackedRows& p, int64_t lo, int64_t hi, int& s)
+{
+    while (s < p.B && p.cu[s + 1] <= lo) ++s;
+    int64_t n = 0;
+    for (int t = s; t < p.B && p.cu[t] < hi; ++t) {
+        if (p.cu[t + 1] == p.cu[t]) continue;
+        const int64_t prefix = (int64_t)(p.cu_k[t + 1] - p.cu_k[t]) - (p.cu[t + 1] - p.cu[t]);
+        n += (prefix + std::min<int64_t>(hi, p.cu[t + 1]) - 1 - p.cu[t]) / kBk + 1;
+    }
+    return n;
+}
+
 // Layout of an inversion over N rows whose selections name nb distinct blocks (nb = ceil(N / B_k)
 // for one sequence; the sum of the sequences' block counts for a packed batch).
 static msa_status layout_fill(int64_t N, int H_kv, int B_k, int k, int64_t nb, int window, int chunk,
-                              msa_kv2q_layout* L)
+                              msa_kv2q_layout* L, const PackedRows* packed = nullptr)
 {
     if (!L || N < 1 || H_kv < 1 || B_k < 1 || k < 1 || window < 0 || chunk < 0 || nb < 1) return MSA_ERR_INVALID_ARG;
     if (B_k != kBk || k > kMaxK || N > kMaxN || nb > (int64_t)kMaxN) return MSA_ERR_UNSUPPORTED;
@@ -249,11 +269,12 @@ static msa_status layout_fill(int64_t N, int H_kv, int B_k, int k, int64_t nb, i
     L->window = window;
     L->chunk = chunk;
     L->n_windows = (int32_t)((N + window - 1) / window);
+    // a block that c of the window's rows select has ceil(c / chunk) items: one more than whole chunks for every visible block
     int64_t max_items = 0;
+    int seq = 0;
     for (int64_t w = 0; w < L->n_windows; ++w) {
         const int64_t lo = w * window, hi = (w + 1) * window < N ? (w + 1) * window : N;
-        const int64_t vis_one = (hi - 1) / B_k + 1; // blocks visible to the window's rows (one sequence)
-        const int64_t vis = vis_one < nb ? vis_one : nb;
+        const int64_t vis = packed ? packed_visible_blocks(*packed, lo, hi, seq) : (hi - 1) / B_k + 1;
         max_items += (int64_t)H_kv * (vis + ((hi - lo) * k + chunk - 1) / chunk);
     }
     L->max_items = max_items;
@@ -824,7 +845,8 @@ struct VarlenWs {
 msa_status varlen_ws(const VarlenPlan& p, int H_q, int H_kv, int d_h, int k, int64_t max_rows_per_pass,
                      size_t workspace_bytes, VarlenWs& w)
 {
-    if (msa_status st = layout_fill(p.T, H_kv, kBk, k, p.NB, 0, 0, &w.L)) return st;
+    const PackedRows rows{p.head.data() + p.off_cu / 4, p.head.data() + p.off_cuk / 4, p.B};
+    if (msa_status st = layout_fill(p.T, H_kv, kBk, k, p.NB, 0, 0, &w.L, &rows)) return st;
     size_t off = kErrBytes;
     w.head = off;
     off += p.head_bytes;
