@@ -427,6 +427,8 @@ MSA_API msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf1
  * blocks block_idx[b][r][0 .. k):
  *   x_j = q[b,h] . K[b,r,j] / sqrt(d_h);  out = sum_j softmax(x)_j V[b,r,j];  lse = log sum_j exp(x_j)
  * A row that sees no key (lens[b] = 0, or no block) gets out = 0 and lse = -inf.
+ * NaN, in q or in rows that are seen, is no error here: it reaches what the formulas let it reach (out and lse
+ * of the heads that read it, the weights of their KV head; a NaN in a row appended makes its 16 elements NaN).
  * w_out != NULL also accumulates the attention weights of every visible position:
  *   w_out[b][r][j] = decay * w_in[b][r][j] + sum over the G heads of softmax(x)_j     for j < lens[b]
  * (the sum is 0 for positions outside the given blocks; w_in = NULL counts as 0; positions from

@@ -1,0 +1,82 @@
+"""The 4-bit cache where its inputs are hard: NaN, scales at the ends of fp32, lists of blocks out of order, memory of
+calls on a stream of their own, and the kernels' rarer instances. Tolerances are those of test_gpu_kv4.py."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import block_sparse_long_idx_b200 as msa  # noqa: E402
+from tests import ref_kv4 as ref  # noqa: E402
+from tests.test_gpu_kv4 import DEVICE_CHECK, check_decode, fill_cache, host_values, i32, make_cache  # noqa: E402
+
+
+# ------------------------------------------------------------------------------------------ NaN
+def check_nan(c, q, lens, out, lse, w_out, w_before, block_idx=None):
+    """out, lse and w_out (of no earlier weights) are NaN where the definition's are, and right elsewhere."""
+    H, d = c.H_kv, c.d_h
+    G = q.shape[1] // H
+    for b, n in enumerate(lens):
+        for r in range(H):
+            pos = np.arange(n)
+            if block_idx is not None:
+                pos = np.concatenate([np.arange(x * 128, min(n, x * 128 + 128)) for x in block_idx[b][r] if x >= 0]).astype(int)
+            K, V = host_values(c, b, r, n)
+            K, V = K[pos], V[pos]
+            hs = slice(r * G, (r + 1) * G)
+            qh = q[b, hs].double().cpu().numpy()
+            want, wl, p, pv, _ = ref.attend(qh, K, V)
+            qa, ka = np.nan_to_num(np.abs(qh)), np.nan_to_num(np.abs(K))
+            e = 2.0 ** -16 * (qa @ ka.T).max() / np.sqrt(d) + 2.0 ** -25 * qa.max() * ka.sum(-1).max() / np.sqrt(d)
+            got = out[b, hs].double().cpu().numpy()
+            assert np.array_equal(np.isnan(got), np.isnan(want)), (b, r)
+            tol = (2.0 ** -11 + 2 * e + 2.0 ** -19) * pv + 2.0 ** -8 * np.abs(want) + 2.0 ** -32 * np.nansum(np.abs(V), 0)
+            ok = ~np.isnan(want)
+            assert (np.abs(got - want)[ok] <= tol[ok]).all(), (b, r)
+            got = lse[b, hs].double().cpu().numpy()
+            assert np.array_equal(np.isnan(got), np.isnan(wl)), (b, r, got)
+            ok = ~np.isnan(wl)
+            assert (np.abs(got - wl)[ok] <= (e + 2.0 ** -22 * np.abs(wl) + 2.0 ** -20)[ok]).all(), (b, r)
+            got = w_out[b, r].double().cpu().numpy()
+            add = np.zeros(n)
+            add[pos] = p.sum(0)
+            assert np.array_equal(np.isnan(got[:n]), np.isnan(add)), (b, r)
+            ok = ~np.isnan(add)
+            assert (np.abs(got[:n] - add)[ok] <= ((2.0 ** -22 + 2 * e + 2.0 ** -19) * add)[ok]).all(), (b, r)
+            assert np.array_equal(got[n:], w_before[b, r, n:].double().cpu().numpy()), "behind the length"
+
+
+@pytest.mark.parametrize("n", [200, 20001], ids=["one_cta", "split"])
+@pytest.mark.parametrize("d, G", [(128, 16), (64, 3)])
+def test_nan(d, G, n):
+    """A NaN in one head's q gives that head NaN, and its KV head's weights; a NaN key gives its KV head NaN; a NaN in V
+    gives NaN in its 16 elements alone. Nothing of it reaches the other heads and sequences, and no row that sees
+    keys says that it sees none (lse = -inf)."""
+    B, H = 2, 4
+    lens = [n, 77]
+    L_max = (n + 127) // 128 * 128
+    g = torch.Generator("cuda").manual_seed(n)
+    c = make_cache(B, L_max, H, d)
+    k = torch.randn((n + 77, H, d), device="cuda", generator=g)
+    v = torch.randn((n + 77, H, d), device="cuda", generator=g)
+    k[n - 3, 1, 5] = float("nan")
+    v[70, 2, d - 1] = float("nan")
+    msa.msa_kv4_append(c, k.bfloat16(), v.bfloat16(), i32([0, 0]), i32([0, n, n + 77]))
+    q = torch.randn((B, H * G, d), device="cuda", generator=g)
+    q[0, 1, 3] = q[1, 3 * G + 2, 0] = float("nan")    # KV heads 0 and 3
+    q = q.bfloat16()
+    before = torch.full((B, H, L_max), 3.0, device="cuda")
+    w_out = before.clone()
+    out, lse = msa.msa_kv4_decode(q, c, i32(lens), weights_out=w_out)
+    check_nan(c, q, lens, out, lse, w_out, before)
+    # given blocks: the NaN key's block is given to KV head 1 of one list and not of the other
+    last = (n - 1) // 128
+    for mine in ([last - 1, last], [last - 1, -1]):
+        sel = np.tile(np.array([0, -1], np.int32), (B, H, 1))
+        sel[0, 1] = mine
+        w_out = before.clone()
+        out, lse = msa.msa_kv4_decode(q, c, i32(lens), torch.from_numpy(sel).cuda(), weights_out=w_out)
+        check_nan(c, q, lens, out, lse, w_out, before, sel)
