@@ -80,3 +80,20 @@ def test_nan(d, G, n):
         w_out = before.clone()
         out, lse = msa.msa_kv4_decode(q, c, i32(lens), torch.from_numpy(sel).cuda(), weights_out=w_out)
         check_nan(c, q, lens, out, lse, w_out, before, sel)
+
+
+# ------------------------------------------------------------------------------------------ eviction of NaN weights
+def test_evict_nan_weights():
+    """A NaN weight counts as the largest whatever its sign, equal to other NaNs: the lower position stays first."""
+    B, H, d, L_max, n, keep = 1, 2, 64, 512, 500, 40
+    c = fill_cache(B, L_max, H, d, [n], seed=3)
+    to = make_cache(B, 128, H, d, (c.k_scale, c.v_scale), fill=0)
+    w = torch.rand((B, H, L_max), device="cuda")
+    w[0, :, 17] = float("inf")
+    bits = w.view(torch.int32)
+    bits[0, 0, 100::7], bits[0, 0, 103::7] = 0x7FC00000, -0x400000        # + and - NaN
+    bits[0, 1, 50:90] = -1                                                # 40 NaNs, all that stay
+    _, kept = msa.msa_kv4_evict(c, to, w, i32([n]), keep)
+    w64 = torch.where(w.isnan(), float("inf"), w.clamp(max=3.0)).double().cpu().numpy()
+    for r in range(H):
+        assert kept[0, r].tolist() == ref.keep_positions(w64[0, r], n, keep, 0, 0).tolist()
