@@ -330,9 +330,9 @@ __device__ __forceinline__ void merge(float& M, float& L, float4& acc, float m, 
 __device__ __forceinline__ void finish(const Kv4DecodeArgs& a, int64_t row, int d, const float4& o, float M, float L)
 {
     // L = 0: no key was seen; a NaN among the logits makes L NaN, and out and lse with it
-    const float inv = L == 0.f ? 0.f : a.v_scale / L;
+    const float inv = L == 0.f ? 0.f : 1.f / L, t = a.v_scale; // t / L may be no normal number where o / L * t is one
     *reinterpret_cast<uint2*>(a.out + row * a.d_h + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        make_uint2(pack_bf16x2(o.x * inv * t, o.y * inv * t), pack_bf16x2(o.z * inv * t, o.w * inv * t));
     if (a.lse && d == 0) a.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * 0.6931471805599453f;
 }
 

@@ -97,3 +97,24 @@ def test_evict_nan_weights():
     w64 = torch.where(w.isnan(), float("inf"), w.clamp(max=3.0)).double().cpu().numpy()
     for r in range(H):
         assert kept[0, r].tolist() == ref.keep_positions(w64[0, r], n, keep, 0, 0).tolist()
+
+
+# ------------------------------------------------------------------------------------------ scales at the ends of fp32
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("v_scale", [2.0 ** -124, 2.0 ** -110, 2.0 ** 110])
+def test_v_scale_range(v_scale, G):
+    """A long flat row, whose sum of P passes 2^22, on a V scale near fp32's ends: outputs are normal numbers there."""
+    B, H, d, n = 1, 1, 64, 40001
+    g = torch.Generator("cuda").manual_seed(G)
+    c = make_cache(B, 40064, H, d, (1.0, v_scale))
+    k = torch.randn((n, H, d), device="cuda", generator=g) * 0.01
+    v = (torch.randn((n, H, d), device="cuda", generator=g) + 4) * v_scale
+    msa.msa_kv4_append(c, k.bfloat16(), v.bfloat16(), i32([0]), i32([0, n]))
+    q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
+    out, _ = msa.msa_kv4_decode(q, c, i32([n]))
+    K, V = host_values(c, 0, 0, n)
+    qh = q[0].double().cpu().numpy()
+    want, _, _, pv, S = ref.attend(qh, K, V)
+    e = 2.0 ** -16 * S + 2.0 ** -25 * np.abs(qh).max() * np.abs(K).sum(-1).max() / np.sqrt(d)
+    tol = (2.0 ** -11 + 2 * e + 2.0 ** -19) * pv + 2.0 ** -8 * np.abs(want) + 2.0 ** -32 * np.abs(V).sum(0)
+    assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
