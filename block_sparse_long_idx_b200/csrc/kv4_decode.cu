@@ -181,7 +181,6 @@ template <int DH, bool NARROW>
 __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int G, int g, int t, uint32_t (&qf)[DH / 16][4],
                                        float& f0, float& f1)
 {
-    const float base = a.k_scale * rsqrtf((float)DH) * 1.4426950408889634f;
 #pragma unroll
     for (int half = 0; half < (NARROW ? 1 : 2); ++half) {
         const int row = g + 8 * half;
@@ -200,8 +199,12 @@ __device__ __forceinline__ void load_q(const Kv4DecodeArgs& a, int b, int r, int
         // 2^e <= mx; e within [-126, 126] so that 2^-e is a normal number too
         const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        // finite and above 0, so that it maps a sum of 0 to 0 and a masked -inf to -inf
-        (half ? f1 : f0) = fminf(fmaxf(base * __uint_as_float((uint32_t)(127 + e) << 23), FLT_MIN), FLT_MAX);
+        // finite and above 0, so that it maps a sum of 0 to 0 and a masked -inf to -inf; a small scale is multiplied by a
+        // large 2^e first (exactly), so that no product on the way is subnormal where the factor is not
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        const bool first = a.k_scale < 1.f && e > 0;
+        const float f = (first ? a.k_scale * up : a.k_scale) * rsqrtf((float)DH) * 1.4426950408889634f;
+        (half ? f1 : f0) = fminf(fmaxf(first ? f : f * up, FLT_MIN), FLT_MAX);
 #pragma unroll
         for (int i = 0; i < DH / 8; ++i) // pair i: elements 2 i, 2 i + 1 of the lane's run
             qf[i / 2][2 * (i & 1) + half] = pack_f16x2(bf16_lo(x[i]) * down, bf16_hi(x[i]) * down);

@@ -118,3 +118,21 @@ def test_v_scale_range(v_scale, G):
     e = 2.0 ** -16 * S + 2.0 ** -25 * np.abs(qh).max() * np.abs(K).sum(-1).max() / np.sqrt(d)
     tol = (2.0 ** -11 + 2 * e + 2.0 ** -19) * pv + 2.0 ** -8 * np.abs(want) + 2.0 ** -32 * np.abs(V).sum(0)
     assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_k_scale_subnormal(d, G):
+    """A subnormal K scale under enormous q: logits of a few units, whose factor keeps all of its bits."""
+    B, H, n = 1, 1, 300
+    g = torch.Generator("cuda").manual_seed(d)
+    c1 = make_cache(B, 384, H, d)
+    k = torch.randint(0, 2049, (n, H, 1), device="cuda", generator=g).float().expand(n, H, d)
+    v = torch.randn((n, H, d), device="cuda", generator=g)
+    msa.msa_kv4_append(c1, k.bfloat16(), v.bfloat16(), i32([0]), i32([0, n]))
+    c = msa.KV4Cache(c1.k_codes, c1.k_scales, c1.v_codes, c1.v_scales, 2.0 ** -140, 1.0)
+    q = torch.linspace(0.5, 1.0, H * G, device="cuda").view(1, -1, 1).expand(B, H * G, d).mul(2.0 ** 127).bfloat16()
+    w_out = torch.zeros((B, H, 384), device="cuda")
+    out, lse = msa.msa_kv4_decode(q, c, i32([n]), weights_out=w_out)
+    assert lse.max() > 6.2  # log(300) is 5.7: the logits count
+    check_decode(c, q, [n], out, lse, w_out=w_out, w_before=torch.zeros_like(w_out))
