@@ -80,14 +80,22 @@ struct Work {
         const int n = blocks(len);
         return n > 0 ? n + kJoin<GIVEN> : 0;
     }
-    // First key of entry i of (b, r); -1 for padding and for entries the check reports.
-    __device__ __forceinline__ int key0(int b, int r, int i, int len) const
+    // First key of entry `lane % 16` of (b, r), by whole warps (the halves may differ in r): -1 for padding and for
+    // entries left out, those outside the sequence and those that do not exceed every block of it before them in the
+    // list (an entry left out for that is below one kept, so all entries inside count). bad: left out, not padding.
+    __device__ __forceinline__ int given_key0(int b, int r, int len, bool& bad) const
     {
-        if (!GIVEN) return i * kBk;
-        const int32_t* sel = a.block_idx + ((int64_t)b * a.H_kv + r) * a.k;
-        const int blk = sel[i];
-        if (blk < 0 || blk > (len - 1) / kBk || (i > 0 && blk <= sel[i - 1])) return -1;
-        return blk * kBk;
+        static_assert(kMaxK <= 16, "a list in 16 lanes");
+        const int i = threadIdx.x & 15;
+        const int blk = i < a.k ? a.block_idx[((int64_t)b * a.H_kv + r) * a.k + i] : -1;
+        const bool inside = blk >= 0 && blk <= (len - 1) / kBk;
+        int top = inside ? blk : -1; // the highest block up to this entry
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_up_sync(0xffffffffu, top, o, 16)); // (itself where there is none)
+        const int before = __shfl_up_sync(0xffffffffu, top, 1, 16);
+        const bool kept = inside && (i == 0 || blk > before);
+        bad = !kept && blk != -1;
+        return kept ? blk * kBk : -1;
     }
 };
 
@@ -169,6 +177,7 @@ struct Shared {
     float m[kSlots][16], l[kSlots][16];
     uint4 q[8][32]; // Q fragments of the segment
     float2 f[32];   // the lanes' factors on its sums (load_q)
+    int key0[16];   // given blocks: the first keys of its list's entries (given_key0)
     int warp_units[kLaunch / 32];
     int b0, seg0; // sequence holding the slice's first unit, first unit of that sequence
     int abort_flag;
@@ -386,10 +395,10 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                 if (a.lse)
                     for (int e = lane; e < a.H_q; e += 32) a.lse[(int64_t)b * a.H_q + e] = -CUDART_INF_F;
             } else if (GIVEN) {
-                for (int e = lane; e < a.H_kv * a.k; e += 32) {
-                    const int r = e / a.k, i = e % a.k;
-                    if (w.key0(b, r, i, len) < 0 && a.block_idx[(int64_t)b * a.H_kv * a.k + e] != -1)
-                        report_error(a.err, MSA_ERR_DEVICE_CHECK, 210);
+                for (int r0 = 0; r0 < a.H_kv; r0 += 2) { // two lists at a time
+                    bool bad;
+                    w.given_key0(b, min(r0 + lane / 16, a.H_kv - 1), len, bad);
+                    if (bad) report_error(a.err, MSA_ERR_DEVICE_CHECK, 210);
                 }
             }
         }
@@ -413,17 +422,19 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
     if (warp >= kWarps) {
         // ---------------------------------------------------------------- producer
         reg_dealloc<kProducerRegs>();
-        if (tid != kThreads) return;
+        if (GIVEN ? warp != kWarps : tid != kThreads) return; // a list of blocks is looked at by a warp
+        const bool first_lane = lane == 0;
         uint32_t n = 0; // chunks
         bool ok = true;
         for (; ok && cons.more(); cons.next_segment(w)) {
             const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
+            bool bad;
+            const int listed = GIVEN && cons.pos < cons.end ? w.given_key0(cons.b, cons.r, cons.len, bad) : -1;
             for (; cons.pos < cons.end; cons.pos += kBlocks, ++n) {
                 const uint32_t st = n % kStages, round = n / kStages;
-                if (round > 0 && !wait_or_abort(&sh.empty[st], (round - 1) & 1, abort_flag, a.err, 62, kWaitLimit)) {
-                    ok = false;
-                    break;
-                }
+                ok = round == 0 || !first_lane || wait_or_abort(&sh.empty[st], (round - 1) & 1, abort_flag, a.err, 62, kWaitLimit);
+                if (GIVEN) ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
                 // up to kBlocks blocks of the segment, the visible rows rounded up to 32 (L_max is whole blocks)
                 uint8_t* s = ring + st * C::STAGE;
                 const int nb = min(kBlocks, cons.end - cons.pos);
@@ -442,18 +453,21 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
                     int key[kBlocks], all = 0;
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i) {
-                        key[i] = i < nb ? w.key0(cons.b, cons.r, cons.pos - cons.seg + i, cons.len) : -1;
+                        key[i] = __shfl_sync(0xffffffffu, listed, (cons.pos - cons.seg + i) & 15);
+                        if (i >= nb) key[i] = -1;
                         if (key[i] >= 0) all += rows_of(key[i], kBk);
                     }
-                    mbar_arrive_expect_tx(&sh.full[st], all * 2 * (C::CODE + C::NG));
+                    if (first_lane) {
+                        mbar_arrive_expect_tx(&sh.full[st], all * 2 * (C::CODE + C::NG));
 #pragma unroll
-                    for (int i = 0; i < kBlocks; ++i)
-                        if (key[i] >= 0) copy(key[i], i * kBk, rows_of(key[i], kBk));
+                        for (int i = 0; i < kBlocks; ++i)
+                            if (key[i] >= 0) copy(key[i], i * kBk, rows_of(key[i], kBk));
+                    }
                 }
             }
         }
         // after an abort, copies may still be in flight: the shared memory must outlive them
-        if (!ok)
+        if (!ok && first_lane)
             for (uint32_t m = n > kStages ? n - kStages : 0; m < n; ++m)
                 drain_wait(&sh.full[m % kStages], (m / kStages) & 1, a.err, 61, kWaitLimit);
         return;
@@ -465,18 +479,23 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
         if (lane == 0) mbar_arrive(&sh.empty[st]);
     };
     // one warp loads a segment's q, for the second and later ones while the segment before is joined
-    auto fetch_q = [&](int b, int r) {
+    auto fetch_q = [&](const Walk<GIVEN>& x) {
         float f0, f1;
         uint32_t qf[DH / 16][4];
-        load_q<DH, NARROW>(a, b, r, G, g, t, qf, f0, f1);
+        load_q<DH, NARROW>(a, x.b, x.r, G, g, t, qf, f0, f1);
         store_q<DH, NARROW>(sh.q, qf, lane);
         sh.f[lane] = make_float2(f0, f1);
+        if (GIVEN) { // and its list of blocks
+            bool bad;
+            const int key = w.given_key0(x.b, x.r, x.len, bad);
+            if (lane < 16) sh.key0[lane] = key;
+        }
     };
     auto to_work = [&](Walk<GIVEN>& x) { // on to a segment with blocks in the slice
         while (x.more() && x.pos >= x.end) x.next_segment(w);
     };
     to_work(cons);
-    if (warp == kWarps - 1 && cons.more()) fetch_q(cons.b, cons.r);
+    if (warp == kWarps - 1 && cons.more()) fetch_q(cons);
     sync_consumers();
     uint32_t used = 0; // chunks
     bool ok = true, first = true;
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
             if (!ok) break;
             int nk = 0; // visible keys of the warp's 32
             if (cons.pos + warp / 4 < cons.end) {
-                const int key = w.key0(cons.b, cons.r, cons.pos + warp / 4 - cons.seg, cons.len);
+                const int i = cons.pos + warp / 4 - cons.seg, key = GIVEN ? sh.key0[i] : i * kBk;
                 if (key >= 0) nk = min(kTile, cons.len - key - kTile * (warp & 3));
             }
             if (nk <= 0) {
@@ -678,7 +697,7 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
             Walk<GIVEN> next = cons;
             next.next_segment(w);
             to_work(next);
-            if (next.more()) fetch_q(next.b, next.r);
+            if (next.more()) fetch_q(next);
         }
         if (warp < kSlots) {
 #pragma unroll
@@ -848,7 +867,10 @@ __global__ void __launch_bounds__(kWThreads, 2) kv4_weights_kernel(Kv4DecodeArgs
         __syncthreads();
         float z0, z1;
         int mine = -1; // given blocks: the first key of this lane's
-        if (GIVEN && lane < a.k) mine = Work<true>{a}.key0(cons.b, cons.r, lane, cons.len);
+        if (GIVEN) {
+            bool bad;
+            mine = Work<true>{a}.given_key0(cons.b, cons.r, cons.len, bad);
+        }
         const int64_t row0 = ((int64_t)cons.b * a.H_kv + cons.r) * a.L_max;
         // the key whose weight ends in this lane (of the sums below)
         const int my_key = NARROW ? 8 * t + (g >> 1) + 4 * (g & 1) : 8 * (g >> 1) + t + 4 * (g & 1), last = min(cons.len, (cons.end - cons.seg) * kBk);

@@ -437,8 +437,9 @@ MSA_API msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf1
  *   lens      : [B] int32 device, 0 <= lens[b] <= L_max, else reported (MSA_ERR_DEVICE_CHECK) and the
  *               sequence's outputs are left unwritten
  *   block_idx : [B, H_kv, k] int32 device (1 <= k <= 16), ascending without repetition, -1 where there
- *               is no block (as msa_sparse_decode gives them), or NULL; other entries are left out and
- *               reported. B_k = 128
+ *               is no block (as msa_sparse_decode gives them), or NULL. Entries outside the sequence, and those
+ *               that do not exceed every block of it before them in the list, are left out and reported (lists of
+ *               a sequence without tokens are not looked at). B_k = 128
  *   w_in, w_out : [B, H_kv, L_max] fp32, the same array or two that do not overlap
  * Sums, softmax statistics and weights are fp32, P and the dequantised values (exact) fp16, out bf16.
  *

@@ -136,3 +136,32 @@ def test_k_scale_subnormal(d, G):
     out, lse = msa.msa_kv4_decode(q, c, i32([n]), weights_out=w_out)
     assert lse.max() > 6.2  # log(300) is 5.7: the logits count
     check_decode(c, q, [n], out, lse, w_out=w_out, w_before=torch.zeros_like(w_out))
+
+
+# ------------------------------------------------------------------------------------------ lists of blocks out of order
+@pytest.mark.parametrize("H", [1, 3])
+@pytest.mark.parametrize("G", [4, 16])
+def test_blocks_given_twice(G, H):
+    """An entry that does not exceed every block before it in its list is left out, from the weights too, and reported;
+    entries outside the sequence do not count for those behind them, nor does padding."""
+    B, d, L_max, n = 2, 128, 1024, 1000
+    lists = [([3, -1, 3, -1], [3]), ([4, 2, 3, 4], [4]), ([2, 0, 2, 7], [2, 7]), ([9, 1, 8, 5], [1, 5]), ([-5, 6, 2 ** 31 - 1, 6], [6]),
+             ([1, 1, 1, 1], [1])]
+    c = fill_cache(B, L_max, H, d, [n, n], seed=8)
+    g = torch.Generator("cuda").manual_seed(9)
+    q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
+    w = torch.rand((B, H, L_max), device="cuda", generator=g)
+    ws = torch.empty(msa.lib.msa_kv4_decode_workspace_size(B, H * G), dtype=torch.uint8, device="cuda")
+    for given, kept in lists:
+        sel = np.tile(np.array([0, 3, 5, -1], np.int32), (B, H, 1))
+        want = sel.copy()
+        sel[1, H - 1] = given
+        want[1, H - 1] = kept + [-1] * (4 - len(kept))
+        w_out = torch.full_like(w, 7.0)
+        out, lse = msa.msa_kv4_decode(q, c, i32([n, n]), torch.from_numpy(sel).cuda(), w, w_out, 0.5, workspace=ws)
+        assert msa.msa_get_device_error(ws) == DEVICE_CHECK, given
+        check_decode(c, q, [n, n], out, lse, want, w, w_out, torch.full_like(w, 7.0), 0.5)
+    sel = np.tile(np.array([0, -1, 1, -1], np.int32), (B, H, 1))     # padding in between
+    out, lse = msa.msa_kv4_decode(q, c, i32([n, n]), torch.from_numpy(sel).cuda(), workspace=ws)
+    assert msa.msa_get_device_error(ws) == 0
+    check_decode(c, q, [n, n], out, lse, sel)
