@@ -1160,6 +1160,9 @@ static msa_status kv4_decode_check(const msa_kv4_cache* c, const void* q, const 
         !aligned(w_in, 4) || !aligned(w_out, 4) || !aligned(workspace, 256) || !std::isfinite(decay) || (w_in && !w_out))
         return MSA_ERR_INVALID_ARG;
     if (w_in != w_out && overlap(w_in, (size_t)kv4_rows(c) * 4, w_out, (size_t)kv4_rows(c) * 4)) return MSA_ERR_INVALID_ARG;
+    // a CTA has read its heads' q before it writes their outputs, but the weights read q again
+    const size_t rows = (size_t)c->B * H_q * c->d_h * 2;
+    if (overlap(q, rows, out, rows) && (q != out || w_out)) return MSA_ERR_INVALID_ARG;
     if (H_q / c->H_kv > 16) return MSA_ERR_UNSUPPORTED;
     return MSA_OK;
 }

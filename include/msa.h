@@ -433,7 +433,8 @@ MSA_API msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf1
  *   w_out[b][r][j] = decay * w_in[b][r][j] + sum over the G heads of softmax(x)_j     for j < lens[b]
  * (the sum is 0 for positions outside the given blocks; w_in = NULL counts as 0; positions from
  * lens[b] on are left as they were).
- *   q, out    : [B, H_q, d_h] bf16, 16-byte aligned;  lse : [B, H_q] fp32, or NULL
+ *   q, out    : [B, H_q, d_h] bf16, 16-byte aligned, apart (without w_out they may be the same array);
+ *               lse : [B, H_q] fp32, or NULL
  *   lens      : [B] int32 device, 0 <= lens[b] <= L_max, else reported (MSA_ERR_DEVICE_CHECK) and the
  *               sequence's outputs are left unwritten
  *   block_idx : [B, H_kv, k] int32 device (1 <= k <= 16), ascending without repetition, -1 where there

@@ -165,3 +165,19 @@ def test_blocks_given_twice(G, H):
     out, lse = msa.msa_kv4_decode(q, c, i32([n, n]), torch.from_numpy(sel).cuda(), workspace=ws)
     assert msa.msa_get_device_error(ws) == 0
     check_decode(c, q, [n, n], out, lse, sel)
+
+
+# ------------------------------------------------------------------------------------------ out in the place of q
+@pytest.mark.parametrize("G", [4, 16])
+def test_out_in_place_of_q(G):
+    """Without weights the outputs may replace q (segments of one CTA, of several)."""
+    B, H, d, L_max = 5, 2, 64, 8064
+    lens = [8000, 1, 700, 0, 4095]
+    c = fill_cache(B, L_max, H, d, lens, seed=14)
+    q = torch.randn((B, H * G, d), device="cuda").bfloat16()
+    x = q.clone()
+    out, lse = msa.msa_kv4_decode(x, c, i32(lens), out=x)
+    assert out is x
+    check_decode(c, q, lens, out, lse)
+    with pytest.raises(msa.MsaError):
+        msa.msa_kv4_decode(x, c, i32(lens), weights_out=torch.zeros((B, H, L_max), device="cuda"), out=x)
