@@ -512,7 +512,8 @@ class KV4Cache:
     nibble), one E4M3 scale per 16 elements [B, H_kv, L_max, d_h / 16] uint8, one fp32 scale per tensor.
 
     L_max is a multiple of 128, d_h 64 or 128. The scales place the format's range: 16-element maxima
-    between 0.1 and 2688 times the scale keep full precision."""
+    between 0.1 and 2688 times the scale keep full precision. The kernels read the addresses and scales given here, so the
+    handle's fields are fixed (the tensors' contents are not); other scales on the same tensors are another KV4Cache."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_scale: float = 1.0, v_scale: float = 1.0):
         if k_codes.dim() != 4:
@@ -522,12 +523,23 @@ class KV4Cache:
         for t, n, last in ((k_codes, "k_codes", half), (k_scales, "k_scales", half // 8), (v_codes, "v_codes", half),
                            (v_scales, "v_scales", half // 8)):
             _is(t, n, (torch.uint8,), (B, H_kv, L_max, last), dev)
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
-        self.B, self.H_kv, self.L_max, self.d_h, self.device = B, H_kv, L_max, 2 * half, dev
-        self._c = msa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), B, H_kv,
-                                2 * half, L_max, self.k_scale, self.v_scale)
-        self._ref = ctypes.byref(self._c)
+        k_scale, v_scale = float(k_scale), float(v_scale)
+        c = msa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), B, H_kv, 2 * half, L_max,
+                          k_scale, v_scale)
+        self.__dict__.update(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, k_scale=k_scale, v_scale=v_scale,
+                             B=B, H_kv=H_kv, L_max=L_max, d_h=2 * half, device=dev, _c=c, _ref=ctypes.byref(c))
+
+    _FIXED = frozenset(("k_codes", "k_scales", "v_codes", "v_scales", "k_scale", "v_scale", "B", "H_kv", "L_max", "d_h", "device", "_c",
+                        "_ref"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED:
+            raise AttributeError(f"KV4Cache.{name} is fixed: make another KV4Cache (it may hold the same tensors)")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+        super().__delattr__(name)
 
     @classmethod
     def empty(cls, B: int, L_max: int, H_kv: int, d_h: int, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda"):
