@@ -20,7 +20,6 @@
 #include "common.cuh"
 #include "mma_sync.cuh"
 #include "sm100.cuh"
-#include "topk.cuh"
 
 namespace msa {
 

@@ -6,7 +6,7 @@
 // L - (k-1) slots hold sentinels (+inf, -1) that nothing can displace, so the admission test is a
 // single compare against the last slot (a static register index, no local memory).
 //
-// Order ("a beats b"): larger score first; equal scores, lower block index first.
+// Order ("a beats b"): larger score first (-inf last); equal scores, lower block index first.
 #pragma once
 #include <cstdint>
 #include <math_constants.h>
@@ -14,11 +14,6 @@
 #include "common.cuh"
 
 namespace msa {
-
-__device__ __forceinline__ bool beats(float v1, int b1, float v2, int b2)
-{
-    return v1 > v2 || (v1 == v2 && b1 < b2);
-}
 
 struct TopkList {
     static constexpr int L = kMaxK - 1;
@@ -31,49 +26,22 @@ struct TopkList {
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const bool sentinel = j < L - k_keep;
-            v[j] = sentinel ? CUDART_INF_F : -CUDART_INF_F;
+            v[j] = sentinel ? CUDART_INF_F : CUDART_NAN_F; // NaN: free
             b[j] = sentinel ? -1 : 0x7FFFFFFF;
         }
     }
 
-    __device__ __forceinline__ bool admits(float val, int blk) const { return beats(val, blk, v[L - 1], b[L - 1]); }
-
-    // Insert (val, blk) keeping the list sorted; the previous last entry falls off.
-    __device__ __forceinline__ void insert(float val, int blk)
-    {
-        bool placed = false;
-#pragma unroll
-        for (int j = L - 1; j >= 0; --j) {
-            if (!placed) {
-                const bool shift = j > 0 && beats(val, blk, v[j - 1], b[j - 1]);
-                if (shift) {
-                    v[j] = v[j - 1];
-                    b[j] = b[j - 1];
-                } else {
-                    v[j] = val;
-                    b[j] = blk;
-                    placed = true;
-                }
-            }
-        }
-    }
-
-    __device__ __forceinline__ void offer(float val, int blk)
-    {
-        if (admits(val, blk)) insert(val, blk);
-    }
-
-    // offer() for a block whose index exceeds that of every listed block (a row's blocks offered in
-    // ascending order): an equal score never beats a listed one, so the order test is a strict
-    // greater-than, and the insertion becomes one independent select per slot (slot j takes its
-    // left neighbour if val beats that, else val if val beats slot j, else keeps its entry) instead
-    // of a serial shift. Sentinels (+inf) are never displaced.
+    // A block whose index exceeds that of every listed block (a row's blocks are offered in ascending order): an equal
+    // score never beats a listed one, so the order test is "not at most", which a free slot's NaN passes for every
+    // score, -inf too: min(k - 1, blocks offered) slots are filled whatever the scores. The insertion is one
+    // independent select per slot (slot j takes its left neighbour if val beats that, else val if val beats slot j,
+    // else keeps its entry) instead of a serial shift. Sentinels (+inf) are never displaced. val is no NaN.
     __device__ __forceinline__ void offer_ascending(float val, int blk)
     {
-        if (!(val > v[L - 1])) return;
+        if (val <= v[L - 1]) return;
         bool c[L];
 #pragma unroll
-        for (int j = 0; j < L; ++j) c[j] = val > v[j];
+        for (int j = 0; j < L; ++j) c[j] = !(val <= v[j]);
 #pragma unroll
         for (int j = L - 1; j >= 1; --j) {
             v[j] = c[j - 1] ? v[j - 1] : (c[j] ? val : v[j]);
