@@ -181,3 +181,73 @@ def test_out_in_place_of_q(G):
     check_decode(c, q, lens, out, lse)
     with pytest.raises(msa.MsaError):
         msa.msa_kv4_decode(x, c, i32(lens), weights_out=torch.zeros((B, H, L_max), device="cuda"), out=x)
+
+
+# ------------------------------------------------------------------------------------------ rarer instances
+@pytest.mark.parametrize("G", [9, 16])
+def test_wide_groups_of_64(G):
+    """d_h 64 with more than 8 heads a KV head: given blocks, and weights with and without them."""
+    B, H, d, k, L_max = 4, 2, 64, 5, 2176
+    lens = [2100, 129, 640, 0]
+    sel = np.full((B, H, k), -1, np.int32)
+    sel[0, 0], sel[0, 1] = [0, 2, 3, 9, 16], [1, 7, -1, -1, -1]
+    sel[1, 0, :2], sel[1, 1, :1] = [0, 1], [1]
+    sel[2, 0, :1] = [4]                                  # sel[2, 1]: nothing
+    c = fill_cache(B, L_max, H, d, lens, seed=G)
+    g = torch.Generator("cuda").manual_seed(G)
+    q = torch.randn((B, H * G, d), device="cuda", generator=g).bfloat16()
+    w = torch.rand((B, H, L_max), device="cuda", generator=g)
+    before = torch.full_like(w, 7.0)
+    for blocks in (None, sel):
+        w_out = before.clone()
+        out, lse = msa.msa_kv4_decode(q, c, i32(lens), None if blocks is None else torch.from_numpy(blocks).cuda(), w, w_out, 0.25)
+        check_decode(c, q, lens, out, lse, blocks, w, w_out, before, 0.25)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_many_rows(d):
+    """Rows enough for several row steps to a reading CTA, the last one ragged."""
+    B, H, L_max = 3, 4, 9088
+    lens, starts = [9001, 4, 8700], [87, 9084, 1]
+    T = sum(lens)
+    g = torch.Generator("cuda").manual_seed(d)
+    x = torch.randn((2, T, H, d), device="cuda", generator=g).bfloat16()
+    c = make_cache(B, L_max, H, d, (0.5, 2.0))
+    cu = i32(np.concatenate([[0], np.cumsum(lens)]))
+    msa.msa_kv4_append(c, x[0], x[1], i32(starts), cu)
+    kr, vr = msa.msa_kv4_read(c, i32(starts), cu, T)
+    for got, src, t in ((kr, x[0], 0.5), (vr, x[1], 2.0)):
+        want = ref.values(*ref.quantise(src.float().cpu().numpy(), t), t)
+        assert torch.equal(got.cpu(), torch.from_numpy(want).float().bfloat16())
+
+
+def test_prefix_of_a_packed_prefill():
+    """Rows read back are the cached prefix of msa_sparse_prefill_varlen: the last row of every chunk selects the blocks
+    of, and attends like, the block-sparse decode of the same position on the cache itself."""
+    B, H, G, d, d_idx, kk, L_max = 3, 2, 4, 128, 32, 4, 1280
+    prefix, chunk = [1024, 0, 384], [200, 77, 640]
+    lens = [p + m for p, m in zip(prefix, chunk)]
+    c = fill_cache(B, L_max, H, d, lens, seed=33)
+    Tk = sum(lens)
+    cu_k = np.concatenate([[0], np.cumsum(lens)])
+    k, v = msa.msa_kv4_read(c, i32([0] * B), i32(cu_k), Tk)
+    g = torch.Generator("cuda").manual_seed(34)
+    T = sum(chunk)
+    cu = np.concatenate([[0], np.cumsum(chunk)])
+    q = torch.randn((T, H * G, d), device="cuda", generator=g).bfloat16()
+    q_idx = torch.randint(-3, 4, (T, H, d_idx), device="cuda", generator=g).bfloat16()
+    k_idx = torch.randint(-3, 4, (Tk, H, d_idx), device="cuda", generator=g).bfloat16()
+    out, lse, sel = msa.msa_sparse_prefill_varlen(q, k, v, q_idx, k_idx, cu, 128, kk, cu_seqlens_k=cu_k)
+    k_idx_cache = torch.zeros((B, L_max, H, d_idx), device="cuda", dtype=torch.bfloat16)
+    for b in range(B):
+        k_idx_cache[b, :lens[b]] = k_idx[cu_k[b]:cu_k[b + 1]]
+    last = torch.from_numpy(cu[1:] - 1).cuda()
+    o, ls, s = msa.msa_sparse_decode_kv4(q[last].contiguous(), q_idx[last].contiguous(), c, k_idx_cache, i32(lens), 128, kk)
+    check_decode(c, q[last], lens, o, ls, s.cpu().numpy())
+    assert torch.equal(sel[:, last].transpose(0, 1), s)
+    # rows are exact in bf16 (6 bits times 1 or 0.75); half steps of 2^-8 of the largest |V|: of the packed form's P twice (itself
+    # and its sum), its partials and both outputs, and one to spare for the rest
+    assert (out[last].float() - o.float()).abs().max() <= 6 * 2.0 ** -8 * v.float().abs().max()
+    # products of at most S = |q| |K| / sqrt(d) in fp32 on both sides
+    S = (q[last].float().norm(dim=-1).max() * k.float().norm(dim=-1).max() / d ** 0.5).item()
+    assert (lse[last] - ls).abs().max() <= 2.0 ** -14 * S + 2.0 ** -18
