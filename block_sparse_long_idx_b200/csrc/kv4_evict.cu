@@ -31,12 +31,12 @@ constexpr int kMaxCluster = 8;           // the portable limit
 __device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : (d == 1 ? 10 : 0); }
 __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 
-// Integers that order like the weights (-0 and +0 are one value, and every NaN is one above +inf).
+// Integers that order like the weights (-0 and +0 are one value, and every NaN is one above +inf), without a branch:
+// the loads of a thread's weights start together.
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
     const uint32_t u = __float_as_uint(w + 0.f);
-    if (w != w) return 0xFFFFFFFFu;
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return (u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) | (w == w ? 0u : 0xFFFFFFFFu);
 }
 
 struct SelShared {
