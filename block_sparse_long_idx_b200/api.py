@@ -8,7 +8,6 @@ If the compiled library is missing the import fails loudly: there is no fallback
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import inspect
@@ -146,36 +145,52 @@ def _workspace(nbytes: int, device, ws):
     return ws
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _side(stream, device):
+def _side(stream):
     """The stream given to a call as torch's, or None where it is the current one."""
-    if stream is None:
-        return None
     handle = _stream(stream)
-    if handle == torch.cuda.current_stream(device).cuda_stream:
+    if handle == torch.cuda.current_stream().cuda_stream:
         return None
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(0 if handle == 1 else handle, device)  # 1: the legacy default stream, torch's 0
+    return torch.cuda.ExternalStream(0 if handle == 1 else handle)  # 1: the legacy default stream, torch's 0
 
 
-def _on(side):
-    """What a call allocates is allocated under the stream that its kernels run on: memory from the current stream's
-    pool may still be in use by work queued there, which the other stream does not wait for."""
-    return _HERE if side is None else torch.cuda.stream(side)
+def _own_tensors(result):
+    if isinstance(result, torch.Tensor):
+        return [result]
+    if isinstance(result, (tuple, list)):
+        return [t for r in result for t in _own_tensors(r)]
+    return [t for t in getattr(result, "__dict__", {}).values() if isinstance(t, torch.Tensor)]
 
 
-def _hold(side, *tensors):
-    """Keeps a call's memory from reuse until both the given stream and the current one, where the caller reads it, are
-    done with it."""
-    if side is None:
-        return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(side)
-            t.record_stream(torch.cuda.current_stream(t.device))
+def _under(side, call, at, args, kw):
+    """The call with `side` as the current stream: what it allocates belongs to that stream, whose kernels use it. (Memory
+    from the pool of the stream that was current may still be in use by work queued there, which `side` does not wait
+    for.) Results are kept from reuse until both streams, as they stand when they are let go of, are done with them."""
+    here = torch.cuda.current_stream(side.device)
+    if len(args) > at:
+        args = args[:at] + (None,) + args[at + 1:]
+    else:
+        kw = {**kw, "stream": None}
+    with torch.cuda.stream(side):
+        result = call(*args, **kw)
+    for t in _own_tensors(result):
+        t.record_stream(side)
+        t.record_stream(here)
+    return result
+
+
+def _on_stream(call):
+    """Runs a call whose `stream` is given and is not the current one under that stream."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        side = None if stream is None else _side(stream)
+        return call(*args, **kw) if side is None else _under(side, call, at, args, kw)
+
+    return run
 
 
 def msa_launch_count() -> int:
@@ -224,6 +239,7 @@ def msa_get_device_error(workspace: torch.Tensor, stream=None) -> int:
     return lib.msa_get_device_error(workspace.data_ptr(), _stream(stream))
 
 
+@_on_stream
 def msa_sparse_prefill_varlen(q, k_, v, q_idx, k_idx, cu_seqlens, B_k: int = 128, k: int = 16, block_idx=None,
                               out=None, lse=None, want_lse: bool = True, workspace=None, max_rows_per_pass: int = 0,
                               stream=None, cu_seqlens_k=None):
@@ -239,50 +255,45 @@ def msa_sparse_prefill_varlen(q, k_, v, q_idx, k_idx, cu_seqlens, B_k: int = 128
     cu_p = cu.ctypes.data_as(ctypes.c_void_p)
     cuk = None if cu_seqlens_k is None else np.ascontiguousarray(np.asarray(cu_seqlens_k, dtype=np.int32))
     cuk_p = None if cuk is None else cuk.ctypes.data_as(ctypes.c_void_p)
+    if block_idx is None:
+        block_idx = torch.empty((H_kv, T, k), dtype=torch.int32, device=q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
     need = lib.msa_sparse_prefill_varlen_workspace_size(cu_p, cuk_p, B, H_q, H_kv, d_h, B_k, k, max_rows_per_pass)
     if need == 0:
         raise MsaError("msa_sparse_prefill_varlen_workspace_size", 1, "arguments rejected")
-    side = _side(stream, q.device)
-    with _on(side):
-        if block_idx is None:
-            block_idx = torch.empty((H_kv, T, k), dtype=torch.int32, device=q.device)
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
-        ws = _workspace(need, q.device, workspace)
+    ws = _workspace(need, q.device, workspace)
     _check("msa_sparse_prefill_varlen", lib.msa_sparse_prefill_varlen(
         q.data_ptr(), k_.data_ptr(), v.data_ptr(), q_idx.data_ptr(), k_idx.data_ptr(), cu_p, cuk_p, B, H_q, H_kv, d_h,
         d_idx,
         B_k, k, block_idx.data_ptr(), out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream)))
-    _hold(side, ws, out, lse, block_idx)
     return out, lse, block_idx
 
 
+@_on_stream
 def msa_selftest_wait_timeout(limit_cycles: int = 1_000_000, workspace=None, device=None, stream=None) -> int:
     """Runs the bounded-wait failure path on the device (a wait that can never complete) and
     returns the device status it left: MSA_ERR_TIMEOUT when the path works."""
     dev = workspace.device if workspace is not None else (device or torch.device("cuda"))
-    with _on(_side(stream, dev)):
-        ws = _workspace(lib.msa_selftest_workspace_size(), dev, workspace)
+    ws = _workspace(lib.msa_selftest_workspace_size(), dev, workspace)
     _check("msa_selftest_wait_timeout", lib.msa_selftest_wait_timeout(ws.data_ptr(), ws.numel(), int(limit_cycles),
                                                                        _stream(stream)))
     return msa_get_device_error(ws, stream)
 
 
+@_on_stream
 def msa_index_topk(q_idx, k_idx, B_k: int = 128, k: int = 16, block_idx=None, workspace=None, stream=None):
     """Index Branch: scores, block max-pool, Top-k with forced local block. Returns block_idx [H_kv, N, k] int32."""
     _bf16(q_idx, "q_idx")
     _bf16(k_idx, "k_idx")
     N, H_kv, d_idx = k_idx.shape
-    side = _side(stream, k_idx.device)
-    with _on(side):
-        if block_idx is None:
-            block_idx = torch.empty((H_kv, N, k), dtype=torch.int32, device=k_idx.device)
-        ws = _workspace(lib.msa_index_topk_workspace_size(N, H_kv, d_idx, B_k, k), k_idx.device, workspace)
+    if block_idx is None:
+        block_idx = torch.empty((H_kv, N, k), dtype=torch.int32, device=k_idx.device)
+    ws = _workspace(lib.msa_index_topk_workspace_size(N, H_kv, d_idx, B_k, k), k_idx.device, workspace)
     _check("msa_index_topk", lib.msa_index_topk(q_idx.data_ptr(), k_idx.data_ptr(), N, H_kv, d_idx, B_k, k,
                                                  block_idx.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
-    _hold(side, ws, block_idx)
     return block_idx
 
 
@@ -319,17 +330,15 @@ class KV2Q:
         return self._i32(self.layout.items, 4 * n).view(n, 4)
 
 
+@_on_stream
 def msa_build_kv2q(block_idx, B_k: int = 128, window: int = 0, chunk: int = 0, workspace=None, stream=None) -> KV2Q:
     """KV->Q inversion of block_idx [H_kv, N, k] into per-block query lists and a work list."""
     H_kv, N, k = block_idx.shape
     L = msa_kv2q_layout_get(N, H_kv, B_k, k, window, chunk)
-    side = _side(stream, block_idx.device)
-    with _on(side):
-        buf = torch.empty(L.total_bytes, dtype=torch.uint8, device=block_idx.device)
-        ws = _workspace(lib.msa_build_kv2q_workspace_size(ctypes.byref(L)), block_idx.device, workspace)
+    buf = torch.empty(L.total_bytes, dtype=torch.uint8, device=block_idx.device)
+    ws = _workspace(lib.msa_build_kv2q_workspace_size(ctypes.byref(L)), block_idx.device, workspace)
     _check("msa_build_kv2q", lib.msa_build_kv2q(block_idx.data_ptr(), ctypes.byref(L), buf.data_ptr(),
                                                  ws.data_ptr(), ws.numel(), _stream(stream)))
-    _hold(side, ws, buf)
     return KV2Q(L, buf)
 
 
@@ -337,6 +346,7 @@ def msa_sparse_prefill_workspace_size(N, H_q, H_kv, d_h, B_k=128, k=16, max_rows
     return lib.msa_sparse_prefill_workspace_size(N, H_q, H_kv, d_h, B_k, k, max_rows_per_pass, int(internal_kv2q))
 
 
+@_on_stream
 def msa_sparse_prefill(q, k_, v, block_idx, kv2q: KV2Q | None = None, B_k: int = 128, out=None, lse=None,
                        want_lse: bool = True, workspace=None, max_rows_per_pass: int = 0, stream=None):
     """Main Branch: exact block-sparse attention on the selected blocks. Returns (out, lse)."""
@@ -345,24 +355,22 @@ def msa_sparse_prefill(q, k_, v, block_idx, kv2q: KV2Q | None = None, B_k: int =
     N, H_q, d_h = q.shape
     H_kv = k_.shape[1]
     kk = block_idx.shape[2]
-    side = _side(stream, q.device)
-    with _on(side):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((N, H_q), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(msa_sparse_prefill_workspace_size(N, H_q, H_kv, d_h, B_k, kk, max_rows_per_pass,
-                                                                      kv2q is None), dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((N, H_q), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(msa_sparse_prefill_workspace_size(N, H_q, H_kv, d_h, B_k, kk, max_rows_per_pass,
+                                                                  kv2q is None), dtype=torch.uint8, device=q.device)
     lp = ctypes.byref(kv2q.layout) if kv2q is not None else None
     _check("msa_sparse_prefill", lib.msa_sparse_prefill(
         q.data_ptr(), k_.data_ptr(), v.data_ptr(), N, H_q, H_kv, d_h, B_k, kk, block_idx.data_ptr(), lp,
         _ptr(kv2q.buf) if kv2q is not None else None, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
         workspace.numel(), _stream(stream)))
-    _hold(side, workspace, out, lse)
     return out, lse
 
 
+@_on_stream
 def msa_sparse_backward(q, k_, v, out, lse, dout, block_idx=None, kv2q: KV2Q | None = None, B_k: int = 128,
                         k: int | None = None, dq=None, dk=None, dv=None, q_idx=None, k_idx=None,
                         kl_weight: float = 1.0, want_kl: bool = True, workspace=None, stream=None):
@@ -383,6 +391,9 @@ def msa_sparse_backward(q, k_, v, out, lse, dout, block_idx=None, kv2q: KV2Q | N
         k = block_idx.shape[2]
     if kv2q is None and block_idx is None:
         raise ValueError("msa_sparse_backward: give block_idx or a built kv2q")
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k_) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     with_kl = q_idx is not None
     d_idx = 0
     dq_idx = dk_idx = kl = None
@@ -392,28 +403,22 @@ def msa_sparse_backward(q, k_, v, out, lse, dout, block_idx=None, kv2q: KV2Q | N
         if block_idx is None:
             raise ValueError("msa_sparse_backward: the KL part needs block_idx")
         d_idx = q_idx.shape[2]
-    side = _side(stream, q.device)
-    with _on(side):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k_) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        if with_kl:
-            dq_idx, dk_idx = torch.empty_like(q_idx), torch.empty_like(k_idx)
-            kl = torch.empty((N, H_kv), dtype=torch.float32, device=q.device) if want_kl else None
-        ws = _workspace(lib.msa_sparse_backward_workspace_size(N, H_q, H_kv, d_h, B_k, k, d_idx, kv2q is None),
-                        q.device, workspace)
+        dq_idx, dk_idx = torch.empty_like(q_idx), torch.empty_like(k_idx)
+        kl = torch.empty((N, H_kv), dtype=torch.float32, device=q.device) if want_kl else None
+    ws = _workspace(lib.msa_sparse_backward_workspace_size(N, H_q, H_kv, d_h, B_k, k, d_idx, kv2q is None),
+                    q.device, workspace)
     lp = ctypes.byref(kv2q.layout) if kv2q is not None else None
     _check("msa_sparse_backward", lib.msa_sparse_backward(
         q.data_ptr(), k_.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), N, H_q, H_kv, d_h,
         B_k, k, _ptr(block_idx), lp, _ptr(kv2q.buf) if kv2q is not None else None, dq.data_ptr(), dk.data_ptr(),
         dv.data_ptr(), _ptr(q_idx), _ptr(k_idx), d_idx, float(kl_weight), _ptr(dq_idx), _ptr(dk_idx), _ptr(kl),
         ws.data_ptr(), ws.numel(), _stream(stream)))
-    _hold(side, ws, dq, dk, dv, dq_idx, dk_idx, kl)
     if with_kl:
         return dq, dk, dv, dq_idx, dk_idx, kl
     return dq, dk, dv
 
 
+@_on_stream
 def msa_sparse_decode(q, q_idx, k_cache, v_cache, k_idx_cache, lens, B_k: int = 128, k: int = 16, out=None, lse=None,
                       want_lse: bool = True, block_idx_out=None, workspace=None, stream=None):
     """Decode: one query per sequence at position lens-1. Returns (out, lse, block_idx)."""
@@ -423,21 +428,18 @@ def msa_sparse_decode(q, q_idx, k_cache, v_cache, k_idx_cache, lens, B_k: int = 
     B, H_q, d_h = q.shape
     L_max, H_kv = k_cache.shape[1], k_cache.shape[2]
     d_idx = q_idx.shape[2]
-    side = _side(stream, q.device)
-    with _on(side):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((B, H_q), dtype=torch.float32, device=q.device)
-        if block_idx_out is None:
-            block_idx_out = torch.empty((B, H_kv, k), dtype=torch.int32, device=q.device)
-        ws = _workspace(lib.msa_sparse_decode_workspace_size(B, L_max, H_q, H_kv, d_h, d_idx, B_k, k), q.device,
-                        workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, H_q), dtype=torch.float32, device=q.device)
+    if block_idx_out is None:
+        block_idx_out = torch.empty((B, H_kv, k), dtype=torch.int32, device=q.device)
+    ws = _workspace(lib.msa_sparse_decode_workspace_size(B, L_max, H_q, H_kv, d_h, d_idx, B_k, k), q.device,
+                    workspace)
     _check("msa_sparse_decode", lib.msa_sparse_decode(
         q.data_ptr(), q_idx.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_idx_cache.data_ptr(),
         lens.data_ptr(), B, L_max, H_q, H_kv, d_h, d_idx, B_k, k, out.data_ptr(), _ptr(lse),
         block_idx_out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
-    _hold(side, ws, out, lse, block_idx_out)
     return out, lse, block_idx_out
 
 
@@ -449,23 +451,22 @@ class E4M3Rows:
         self.codes, self.scales, self.rscales, self.blkmax = codes, scales, rscales, blkmax
 
 
+@_on_stream
 def msa_quantize_e4m3(x, with_rscales: bool = True, with_blkmax: bool = True, stream=None) -> E4M3Rows:
     """E4M3 codes and per-row scales (amax / 448) of x [N, H, d] bf16."""
     _bf16(x, "x")
     N, H, d = x.shape
     S = (N + 127) // 128 * 128
-    side = _side(stream, x.device)
-    with _on(side):
-        codes = torch.empty((N, H, d), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((H, S), dtype=torch.float32, device=x.device)
-        rscales = torch.empty((H, S), dtype=torch.float32, device=x.device) if with_rscales else None
-        blkmax = torch.empty((H, S // 128), dtype=torch.float32, device=x.device) if with_blkmax else None
+    codes = torch.empty((N, H, d), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((H, S), dtype=torch.float32, device=x.device)
+    rscales = torch.empty((H, S), dtype=torch.float32, device=x.device) if with_rscales else None
+    blkmax = torch.empty((H, S // 128), dtype=torch.float32, device=x.device) if with_blkmax else None
     _check("msa_quantize_e4m3", lib.msa_quantize_e4m3(x.data_ptr(), N, H, d, codes.data_ptr(), scales.data_ptr(),
                                                        _ptr(rscales), _ptr(blkmax), _stream(stream)))
-    _hold(side, codes, scales, rscales, blkmax)
     return E4M3Rows(codes, scales, rscales, blkmax)
 
 
+@_on_stream
 def msa_sparse_prefill_fp8(q8: E4M3Rows, k8: E4M3Rows, v8: E4M3Rows, block_idx, kv2q: KV2Q | None = None,
                            B_k: int = 128, out=None, lse=None, want_lse: bool = True, workspace=None,
                            max_rows_per_pass: int = 0, stream=None):
@@ -473,23 +474,20 @@ def msa_sparse_prefill_fp8(q8: E4M3Rows, k8: E4M3Rows, v8: E4M3Rows, block_idx, 
     N, H_q, d_h = q8.codes.shape
     H_kv = k8.codes.shape[1]
     kk = block_idx.shape[2]
-    side = _side(stream, q8.codes.device)
-    with _on(side):
-        if out is None:
-            out = torch.empty((N, H_q, d_h), dtype=torch.bfloat16, device=q8.codes.device)
-        if lse is None and want_lse:
-            lse = torch.empty((N, H_q), dtype=torch.float32, device=q8.codes.device)
-        if workspace is None:
-            workspace = torch.empty(msa_sparse_prefill_workspace_size(N, H_q, H_kv, d_h, B_k, kk, max_rows_per_pass,
-                                                                      kv2q is None), dtype=torch.uint8,
-                                    device=q8.codes.device)
+    if out is None:
+        out = torch.empty((N, H_q, d_h), dtype=torch.bfloat16, device=q8.codes.device)
+    if lse is None and want_lse:
+        lse = torch.empty((N, H_q), dtype=torch.float32, device=q8.codes.device)
+    if workspace is None:
+        workspace = torch.empty(msa_sparse_prefill_workspace_size(N, H_q, H_kv, d_h, B_k, kk, max_rows_per_pass,
+                                                                  kv2q is None), dtype=torch.uint8,
+                                device=q8.codes.device)
     lp = ctypes.byref(kv2q.layout) if kv2q is not None else None
     _check("msa_sparse_prefill_fp8", lib.msa_sparse_prefill_fp8(
         q8.codes.data_ptr(), q8.scales.data_ptr(), k8.codes.data_ptr(), k8.scales.data_ptr(), v8.codes.data_ptr(),
         v8.scales.data_ptr(), v8.rscales.data_ptr(), v8.blkmax.data_ptr(), N, H_q, H_kv, d_h, B_k, kk,
         block_idx.data_ptr(), lp, _ptr(kv2q.buf) if kv2q is not None else None, out.data_ptr(), _ptr(lse),
         workspace.data_ptr(), workspace.numel(), _stream(stream)))
-    _hold(side, workspace, out, lse)
     return out, lse
 
 
@@ -526,11 +524,12 @@ class KV4Cache:
         k_scale, v_scale = float(k_scale), float(v_scale)
         c = msa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), B, H_kv, 2 * half, L_max,
                           k_scale, v_scale)
-        self.__dict__.update(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, k_scale=k_scale, v_scale=v_scale,
-                             B=B, H_kv=H_kv, L_max=L_max, d_h=2 * half, device=dev, _c=c, _ref=ctypes.byref(c))
+        fields = dict(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, k_scale=k_scale, v_scale=v_scale, B=B,
+                      H_kv=H_kv, L_max=L_max, d_h=2 * half, device=dev, _c=c, _ref=ctypes.byref(c))
+        for name in self._FIXED:
+            super().__setattr__(name, fields[name])
 
-    _FIXED = frozenset(("k_codes", "k_scales", "v_codes", "v_scales", "k_scale", "v_scale", "B", "H_kv", "L_max", "d_h", "device", "_c",
-                        "_ref"))
+    _FIXED = ("k_codes", "k_scales", "v_codes", "v_scales", "k_scale", "v_scale", "B", "H_kv", "L_max", "d_h", "device", "_c", "_ref")
 
     def __setattr__(self, name, value):
         if name in self._FIXED:
@@ -552,16 +551,19 @@ class KV4Cache:
 
 def _on_device(call):
     """Runs a call of this section, whose tensors live on the device of its KV4Cache argument, with that device
-    current (the library launches on the current device)."""
-    at = list(inspect.signature(call).parameters).index("cache")
+    current (the library launches on the current device), and under the given stream (_under)."""
+    names = list(inspect.signature(call).parameters)
+    at, at_stream = names.index("cache"), names.index("stream")
 
     @functools.wraps(call)
     def run(*args, **kw):
         device = (args[at] if len(args) > at else kw["cache"]).device
-        if device.index == torch.cuda.current_device():
-            return call(*args, **kw)
-        with torch.cuda.device(device):
-            return call(*args, **kw)
+        if device.index != torch.cuda.current_device():
+            with torch.cuda.device(device):
+                return run(*args, **kw)
+        stream = args[at_stream] if len(args) > at_stream else kw.get("stream")
+        side = None if stream is None else _side(stream)
+        return call(*args, **kw) if side is None else _under(side, call, at_stream, args, kw)
 
     return run
 
@@ -618,21 +620,18 @@ def msa_kv4_read(cache: KV4Cache, starts, cu_seqlens=None, T: int | None = None,
         T = cache.B
     _tables(cache, T, starts, cu_seqlens)
     shape = (T, cache.H_kv, cache.d_h)
-    side = _side(stream, cache.device)
-    with _on(side):
-        if k is None:
-            k = torch.empty_strided(shape, (cache.H_kv * cache.d_h, cache.d_h, 1), dtype=torch.bfloat16, device=cache.device)
-        else:
-            _is(k, "k", _BF16, shape, cache.device)
-        if v is None:
-            v = torch.empty_like(k)
-        else:
-            _is(v, "v", _BF16, shape, cache.device)
+    if k is None:
+        k = torch.empty_strided(shape, (cache.H_kv * cache.d_h, cache.d_h, 1), dtype=torch.bfloat16, device=cache.device)
+    else:
+        _is(k, "k", _BF16, shape, cache.device)
+    if v is None:
+        v = torch.empty_like(k)
+    else:
+        _is(v, "v", _BF16, shape, cache.device)
     ws = None if workspace is None else _workspace(lib.msa_kv4_rows_workspace_size(), cache.device, workspace)
     _check("msa_kv4_read", lib.msa_kv4_read(
         cache._ref, k.data_ptr(), v.data_ptr(), T, starts.data_ptr(), _ptr(cu_seqlens), _ptr(ws), 0 if ws is None else ws.numel(),
         _raw_stream(cache.device, stream)))
-    _hold(side, k, v)
     return k, v
 
 
@@ -678,17 +677,14 @@ def msa_kv4_decode(q, cache: KV4Cache, lens, block_idx=None, weights=None, weigh
             raise ValueError("block_idx: expected [B, H_kv, k]")
         k = block_idx.shape[2]
         _is(block_idx, "block_idx", _I32, (cache.B, cache.H_kv, k), cache.device)
-    side = _side(stream, cache.device)
-    with _on(side):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty_strided((cache.B, H_q), (H_q, 1), dtype=torch.float32, device=cache.device)
-        ws = _workspace(_kv4_decode_bytes(cache.B, H_q), cache.device, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty_strided((cache.B, H_q), (H_q, 1), dtype=torch.float32, device=cache.device)
+    ws = _workspace(_kv4_decode_bytes(cache.B, H_q), cache.device, workspace)
     _check("msa_kv4_decode", lib.msa_kv4_decode(
         cache._ref, q.data_ptr(), lens.data_ptr(), H_q, _ptr(block_idx), k, _ptr(weights), _ptr(weights_out), decay,
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _raw_stream(cache.device, stream)))
-    _hold(side, ws, out, lse)
     return out, lse
 
 
@@ -706,20 +702,17 @@ def msa_sparse_decode_kv4(q, q_idx, cache: KV4Cache, k_idx_cache, lens, B_k: int
     _is(k_idx_cache, "k_idx_cache", _BF16, (cache.B, cache.L_max, cache.H_kv, d_idx), cache.device)
     if block_idx_out is not None:
         _is(block_idx_out, "block_idx_out", _I32, (cache.B, cache.H_kv, k), cache.device)
-    side = _side(stream, cache.device)
-    with _on(side):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty_strided((cache.B, H_q), (H_q, 1), dtype=torch.float32, device=cache.device)
-        if block_idx_out is None:
-            block_idx_out = torch.empty((cache.B, cache.H_kv, max(k, 0)), dtype=torch.int32, device=cache.device)
-        ws = _workspace(_sparse_decode_kv4_bytes(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k), cache.device, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty_strided((cache.B, H_q), (H_q, 1), dtype=torch.float32, device=cache.device)
+    if block_idx_out is None:
+        block_idx_out = torch.empty((cache.B, cache.H_kv, max(k, 0)), dtype=torch.int32, device=cache.device)
+    ws = _workspace(_sparse_decode_kv4_bytes(cache.B, cache.L_max, H_q, cache.H_kv, B_k, k), cache.device, workspace)
     _check("msa_sparse_decode_kv4", lib.msa_sparse_decode_kv4(
         cache._ref, q.data_ptr(), q_idx.data_ptr(), k_idx_cache.data_ptr(), lens.data_ptr(), H_q, d_idx, B_k, k,
         _ptr(weights), _ptr(weights_out), decay, out.data_ptr(), _ptr(lse), block_idx_out.data_ptr(), ws.data_ptr(),
         ws.numel(), _raw_stream(cache.device, stream)))
-    _hold(side, ws, out, lse, block_idx_out)
     return out, lse, block_idx_out
 
 
@@ -750,17 +743,14 @@ def msa_kv4_evict(cache: KV4Cache, to: KV4Cache, weights, lens, keep: int, recen
         _is(lens_out, "lens_out", _I32, (cache.B,), dev)
     if kept is not None:
         _is(kept, "kept", _I32, (cache.B, cache.H_kv, keep), dev)
-    side = _side(stream, dev)
-    with _on(side):
-        if lens_out is None:
-            lens_out = torch.empty_like(lens)
-        if kept is None:
-            keep_ = max(keep, 0)
-            kept = torch.empty_strided((cache.B, cache.H_kv, keep_), (cache.H_kv * keep_, keep_, 1), dtype=torch.int32, device=dev)
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if kept is None:
+        keep_ = max(keep, 0)
+        kept = torch.empty_strided((cache.B, cache.H_kv, keep_), (cache.H_kv * keep_, keep_, 1), dtype=torch.int32, device=dev)
     ws = None if workspace is None else _workspace(lib.msa_kv4_evict_workspace_size(cache.B, cache.H_kv, keep), dev, workspace)
     _check("msa_kv4_evict", lib.msa_kv4_evict(
         cache._ref, to._ref, weights.data_ptr(), lens.data_ptr(), keep, recent, first, _ptr(k_idx_cache), _ptr(k_idx_dst),
         d_idx, _ptr(weights_dst), lens_out.data_ptr(), kept.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
         _raw_stream(dev, stream)))
-    _hold(side, lens_out, kept)
     return lens_out, kept
