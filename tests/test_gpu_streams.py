@@ -105,3 +105,29 @@ def test_freed_memory_of_the_current_stream_is_not_taken():
                 assert (x.contiguous().view(torch.uint8) != 0x55).any(), name
             else:
                 assert torch.equal(x, y), name
+
+
+def test_given_stream_in_a_capture():
+    """Calls on a stream that a capture has forked to are captured with it; the graph holds their memory over replays."""
+    calls = {n: f for n, f in make_calls().items() if n not in ("varlen", "backward")}  # (host copies; unordered additions)
+    want = {n: [t.clone() for t in f(None)] for n, f in calls.items()}
+    side = torch.cuda.Stream()
+    for f in calls.values():
+        f(side)
+    torch.cuda.synchronize()
+    graph, got = torch.cuda.CUDAGraph(), {}
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        for n, f in calls.items():
+            got[n] = list(f(side))
+        here.wait_stream(side)
+    for _ in range(2):
+        for v in got.values():
+            for t in v:
+                t.view(torch.uint8).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in calls:
+            for x, y in zip(got[n], want[n]):
+                assert torch.equal(x, y), n
