@@ -12,7 +12,8 @@
 //            Bound by the latency of its rounds: 16 sequences in [20K, 32K] take 21 us, where reading the
 //            weights takes 1.
 //   move   : CTAs of 64 kept rows; a thread starts all its loads before its stores. Bound by memory: 4096 rows of
-//            each, with index keys of 64, take 28 us (5.6 TB/s; kept rows lie 72 and 128 bytes at a time).
+//            each, with index keys of 64, take 30 us (5.2 TB/s in the capture, which reads 126 MB for 72 MB
+//            of rows: a row's scales are 8 bytes of a 32-byte sector, a weight 4).
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"

@@ -408,8 +408,8 @@ typedef struct {
  * Rows that the tables put outside the cache or outside [cu_seqlens[0], cu_seqlens[B]) are left out
  * and reported (MSA_ERR_DEVICE_CHECK). No other row of the cache changes.
  *
- * msa_kv4_read: the same rows back, as bf16 values: k, v [T, H_kv, d_h], contiguous (rows left out as
- * above are not written). What msa_sparse_prefill_varlen takes as cached prefixes.
+ * msa_kv4_read: the same rows back, as bf16 values (code * scale, exact, times t in fp32, rounded to bf16):
+ * k, v [T, H_kv, d_h], contiguous (rows left out as above are not written). What msa_sparse_prefill_varlen takes as cached prefixes.
  */
 MSA_API size_t msa_kv4_rows_workspace_size(void);
 
@@ -429,6 +429,7 @@ MSA_API msa_status msa_kv4_read(const msa_kv4_cache* cache, msa_bf16* k, msa_bf1
  * A row that sees no key (lens[b] = 0, or no block) gets out = 0 and lse = -inf.
  * NaN, in q or in rows that are seen, is no error here: it reaches what the formulas let it reach (out and lse
  * of the heads that read it, the weights of their KV head; a NaN in a row appended makes its 16 elements NaN).
+ * Logits have to fit fp32 (times log2 e); those of finite q and rows that do not may give NaN.
  * w_out != NULL also accumulates the attention weights of every visible position:
  *   w_out[b][r][j] = decay * w_in[b][r][j] + sum over the G heads of softmax(x)_j     for j < lens[b]
  * (the sum is 0 for positions outside the given blocks; w_in = NULL counts as 0; positions from
