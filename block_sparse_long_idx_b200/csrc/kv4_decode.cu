@@ -17,8 +17,9 @@
 // The heads of a KV head are the 16 rows of mma.sync m16n8k16, or with up to 8 heads the 8 columns. (As rows they would
 // fill an eighth of a tcgen05 tile; keys as its 128 rows and heads as its columns would fill it, with K converted into
 // an operand in shared or tensor memory first, where here codes become fragments in registers: not built.)
-// No pipe is saturated: issue 52 %, tensor 41 %, DRAM 48 % in the capture of 8 sequences in [16K, 128K]; the kernels
-// of 9 to 16 heads of 128 spill (116 bytes of stores for all keys, 188 for given blocks), the others do not.
+// No pipe is saturated: issue 52 %, tensor 40 %, DRAM 48 % in the capture of 8 sequences in [16K, 128K]; the kernels
+// of 9 to 16 heads of 128 spill (116 bytes of stores for all keys, 188 for given blocks, 36 in their weights), the
+// others do not.
 // E2M1 codes become fp16 pairs with the hardware conversion, times the E4M3 scale
 // (both exact); no step goes through shared memory, because both products may sum in any order:
 //   S = Q K^T: lane (g, t) holds d_h / 4 consecutive codes of key row g, so element t * d_h / 4 + 4 ks
@@ -760,8 +761,8 @@ __global__ void __launch_bounds__(kLaunch, 1) kv4_decode_kernel(Kv4DecodeArgs a)
 // Joins the partials of the segments that several CTAs share. CTA (c, y): the segment whose first block is in
 // CTA c's slice and whose last is not (there is at most one), heads kJoinRows y and on; kJoinGroups warps a
 // head, each with every kJoinGroups-th partial, in a fixed order. Bound by latency (37 partials of 16 heads for each
-// KV head of one long sequence): an SM has registers for it once its attention CTA, which holds all of them, has left, so its start overlaps the
-// attention's last CTAs only.
+// KV head of one long sequence). It is launched early, but an SM has registers for it only once its attention CTA, which
+// holds all of them, has left: its start overlaps the attention's last CTAs.
 constexpr int kJoinRows = 4, kJoinGroups = 4, kJoinThreads = kJoinRows * kJoinGroups * 32;
 
 template <int DH, bool GIVEN>

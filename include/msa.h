@@ -409,7 +409,8 @@ typedef struct {
  * and reported (MSA_ERR_DEVICE_CHECK). No other row of the cache changes.
  *
  * msa_kv4_read: the same rows back, as bf16 values (code * scale, exact, times t in fp32, rounded to bf16):
- * k, v [T, H_kv, d_h], contiguous (rows left out as above are not written). What msa_sparse_prefill_varlen takes as cached prefixes.
+ * k, v [T, H_kv, d_h], contiguous (rows left out as above are not written). What msa_sparse_prefill_varlen
+ * takes as cached prefixes.
  */
 MSA_API size_t msa_kv4_rows_workspace_size(void);
 
@@ -467,7 +468,8 @@ MSA_API msa_status msa_sparse_decode_kv4(const msa_kv4_cache* cache, const msa_b
  * msa_kv4_evict: copies what is kept of every (sequence, KV head) to the front of another cache. Of n =
  * lens[b] tokens all stay when n <= keep; otherwise the first `first`, the last `recent` and, of the
  * others, those with the largest accumulated weight w[b][r][j] (equal weights: the lower position; a NaN
- * is larger than any number, and equal to other NaNs) stay, `keep` in all, in their order. KV heads keep different tokens; every one keeps the same number.
+ * is larger than any number, and equal to other NaNs) stay, `keep` in all, in their order. KV heads keep
+ * different tokens; every one keeps the same number.
  *   to       : the other cache: the same B, H_kv, d_h, k_scale and v_scale, L_max >= keep; no overlap
  *   w        : [B, H_kv, cache->L_max] fp32;  w_to : [B, H_kv, to->L_max] fp32 out, or NULL
  *   k_idx    : [B, cache->L_max, H_kv, d_idx] bf16 index keys, 16-byte aligned, or NULL (d_idx = 0, k_idx_to
